@@ -23,6 +23,11 @@
 // the logit (K) and the weight (V); since a page's weight times its scale is
 // what is rounded, m refers to logit + log2(V scale).
 //
+// Over a bf16 cache a weight is the sum of two bf16 numbers, to 2^-16 of it, in
+// columns of their own likewise.  The second costs nothing where the cache's
+// bytes are the bound: 16 sequences of 65 to 4160 keys take 89.0 us with one
+// term, 89.5 with two.
+//
 // m grows only when a weight would pass 2^SLACK: then the four softmax warps
 // agree on new references and rescale O in tensor memory.  Otherwise a tile
 // costs them one barrier.
@@ -101,8 +106,10 @@ struct Shape {
     static constexpr int THREADS = 32 * (2 + 5 * GROUPS);  // and a producer and a query warp
     static constexpr int SOFT = 1 + GROUPS, QUERY = 1 + 5 * GROUPS;  // first softmax warp, query warp
     static constexpr int QD = RB == 2 ? 3 : 2;             // items whose queries are in shared memory
-    static constexpr int TERMS = FP8 ? 2 : 1;
-    static constexpr int N = TERMS * RW < 16 ? 16 : TERMS * RW;  // columns of a group's S^T and O^T
+    static constexpr int TERMS = FP8 ? 2 : 1;    // numbers that a query's element is split into
+    static constexpr int WTERMS = 2;             // and a weight
+    static constexpr int NS = TERMS * RW < 16 ? 16 : TERMS * RW;    // columns of a group's S^T
+    static constexpr int NO = WTERMS * RW < 16 ? 16 : WTERMS * RW;  // and O^T
     // A bf16 tile of head_dim 128 goes through the ring of slots as its K part
     // and its V part, others whole.  A part is C columns of 128 bytes; 8 keys of
     // column 0, the same keys of column 1, .., then the next 8 keys.
@@ -113,20 +120,25 @@ struct Shape {
     static constexpr uint32_t VCOL = !FP8 || D == 64 ? 0 : 1024; // first column of M in O^T (see the epilogue for 64)
     static constexpr int QBOXES = D * EB < 128 ? 1 : D * EB / 128;
     // Rows of a group's queries' and weights' operands that exist; the columns
-    // past TERMS * RW read whatever follows and are never looked at.
-    static constexpr int ROWS = TERMS * RW < 8 ? 8 : TERMS * RW;
+    // past the terms of RW rows read whatever follows and are never looked at.
+    static constexpr int QROWS = TERMS * RW < 8 ? 8 : TERMS * RW;
+    static constexpr int PROWS = WTERMS * RW < 8 ? 8 : WTERMS * RW;
     static constexpr int PBOXES = kTile * EB / 128;
-    static constexpr uint32_t QGROUP = QBOXES * ROWS * 128, PGROUP = PBOXES * ROWS * 128;
+    static constexpr uint32_t QGROUP = QBOXES * QROWS * 128, PGROUP = PBOXES * PROWS * 128;
     static constexpr uint32_t QBUF = GROUPS * QGROUP, PBUF = GROUPS * PGROUP;
-    static constexpr int TMEM = 4 * N * GROUPS;                  // S^T twice, O^T twice
+    static constexpr int GCOLS = 2 * (NS + NO);                  // of a group: S^T twice, O^T twice
+    static constexpr int TCOLS = GCOLS * GROUPS;
+    static constexpr int TMEM = TCOLS <= 64 ? 64 : TCOLS <= 128 ? 128 : TCOLS <= 256 ? 256 : 512;
     // log2 of how far a weight may pass 1 before the references move, and of
     // the factor that weights are held with (E4M3 reaches 448).
     static constexpr int SLACK = FP8 ? 3 : 8;
     static constexpr int HELD = FP8 ? 8 - SLACK : 0;
     static constexpr int PIECE = RB * (D + 2);  // floats of a published piece: O, m, l
     // Few rows leave the tensor cores idle while a tile's weights are made:
-    // other CTAs of the SM fill in.
-    static constexpr int CTAS = RB <= 8 || (RB == 16 && D * EB < 256) ? 2 : 1;
+    // other CTAs of the SM fill in.  In bf16 a block of 16 takes one CTA with
+    // 6 slots instead of two with 2: 32 sequences x 4000 keys, 64 heads over 4
+    // of 64, 37.5 us and 39.4; 4 x 20000 keys 32.5 and 35.3.
+    static constexpr int CTAS = RB <= 8 || (RB == 16 && FP8) ? 2 : 1;
     static constexpr uint32_t ROWF = (3 * QD + 8 + 8 + 2) * (RB < 8 ? 8 : RB);  // qc, bound, orow [QD], wmax, lsum [2][4], m [2]
     static constexpr uint32_t FIXED = QD * QBUF + 2 * PBUF + kBarBytes + kScaleRing * 64 + ROWF * 4 + QD * sizeof(Info) + 16 + 1024;
     static constexpr uint32_t ROOM = (228 * 1024) / CTAS - 1024 - 256;
@@ -139,7 +151,7 @@ struct Shape {
     static constexpr uint32_t OFF_INFO = OFF_ROW + ROWF * 4;
     static constexpr uint32_t SMEM = OFF_INFO + QD * sizeof(Info) + 16 + 1024;  // TMEM address, flags; alignment slack
     static_assert(SLOTS >= PARTS + 1 && (2 * SLOTS + 7 * GROUPS + 2 * QD) * 8 <= (int)kBarBytes, "slots of K and V");
-    static_assert(SMEM <= ROOM && TMEM * CTAS <= 512, "shared and tensor memory of a CTA");
+    static_assert(SMEM <= ROOM && TCOLS <= TMEM && TMEM * CTAS <= 512, "shared and tensor memory of a CTA");
 };
 
 template <int RB>
@@ -391,10 +403,10 @@ __device__ __forceinline__ void sts128(uint32_t a, const uint4 &v)
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// Columns (rows of a group) c0 .. c0 + n - 1 at `col` of S^T or O^T, their
-// terms joined: n = 8, or 16 with fewer waits.
+// Columns (rows of a group) c0 .. c0 + n - 1 at `col` of S^T, the terms of
+// their queries joined: n = 8, or 16 with fewer waits.
 template <bool FP8, int RW, int n>
-__device__ __forceinline__ void load_terms(uint32_t col, float (&x)[n])
+__device__ __forceinline__ void load_logits(uint32_t col, float (&x)[n])
 {
     if constexpr (!FP8) {
         if constexpr (n == 8)
@@ -410,6 +422,23 @@ __device__ __forceinline__ void load_terms(uint32_t col, float (&x)[n])
         tmem_ld_pair(col, col + RW, x, y);
 #pragma unroll
         for (int i = 0; i < n; ++i) x[i] = fmaf(y[i], 0.0625f, x[i]);
+    }
+}
+
+// 8 columns of O^T at `col`, the terms of their weights joined.
+template <bool FP8, int RW>
+__device__ __forceinline__ void load_out(uint32_t col, float (&x)[8])
+{
+    constexpr float second = FP8 ? 0.0625f : 1.f;
+    if constexpr (RW < 8) {
+        tmem_ld8(col, x);
+#pragma unroll
+        for (int i = 0; i < RW; ++i) x[i] = fmaf(x[RW + i], second, x[i]);
+    } else {
+        float y[8];
+        tmem_ld_pair(col, col + RW, x, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = fmaf(y[i], second, x[i]);
     }
 }
 
@@ -647,7 +676,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
     attn_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttnParams p)
 {
     using S = Shape<FP8, D, RB>;
-    constexpr int N = S::N, SLOTS = S::SLOTS;
+    constexpr int NS = S::NS, NO = S::NO, SLOTS = S::SLOTS;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -715,10 +744,10 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
         // MMA warp of a group: all lanes keep the (uniform) books, one elected lane
         // issues; a lone lane in a branch would make the compiler move every
         // operand to the uniform registers inside it, MMA by MMA.
-        constexpr uint32_t id_s = FP8 ? idesc_e4m3_f32(128, N) : idesc_bf16_f32(128, N);
-        constexpr uint32_t id_o = id_s | kIdescAMMajor;
+        constexpr uint32_t id_s = FP8 ? idesc_e4m3_f32(128, NS) : idesc_bf16_f32(128, NS);
+        constexpr uint32_t id_o = (FP8 ? idesc_e4m3_f32(128, NO) : idesc_bf16_f32(128, NO)) | kIdescAMMajor;
         const bool leader = elect_one();
-        const uint32_t s_col = tmem + group * 4 * N, o_col = s_col + 2 * N;
+        const uint32_t s_col = tmem + group * S::GCOLS, o_col = s_col + 2 * NS;
         int g = 0, taken = 0, slot_before = 0;
         bool ok = true, first_before = false;
         uint32_t o_before = 0;
@@ -746,7 +775,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
 #pragma unroll
                 for (int s = 0; s < kTile * S::EB / 32; ++s)
                     mma(o_before, vd + (uint64_t)(s * (32 / S::EB / 8) * S::SBO / 16),
-                        pd + (uint64_t)((s / 4 * S::ROWS * 128 + s % 4 * 32) / 16), id_o, !(first_before && s == 0));
+                        pd + (uint64_t)((s / 4 * S::PROWS * 128 + s % 4 * 32) / 16), id_o, !(first_before && s == 0));
                 umma_commit(empty + 8 * st);
                 umma_commit(pv_done + 8 * b);
             }
@@ -770,8 +799,8 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                 if (leader) {
 #pragma unroll
                     for (int s = 0; s < D * S::EB / 32; ++s)
-                        mma(s_col + (g & 1) * N, kd + (uint64_t)((s / 4 * 1024 + s % 4 * 32) / 16),
-                            qd + (uint64_t)((s / 4 * S::ROWS * 128 + s % 4 * 32) / 16), id_s, s > 0);
+                        mma(s_col + (g & 1) * NS, kd + (uint64_t)((s / 4 * 1024 + s % 4 * 32) / 16),
+                            qd + (uint64_t)((s / 4 * S::QROWS * 128 + s % 4 * 32) / 16), id_s, s > 0);
                     if (S::PARTS == 2) umma_commit(empty + 8 * st);
                     umma_commit(s_full + 8 * (g & 1));
                 }
@@ -779,7 +808,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                 if (g > 0 && !(ok = values(g - 1))) break;
                 slot_before = st;
                 first_before = t == t0;
-                o_before = o_col + (k & 1) * N;
+                o_before = o_col + (k & 1) * NO;
                 ++g;
             }
         }
@@ -839,7 +868,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                         }
                     } else if (r < nr) {
                         const int r1 = r < half ? r : r - half;
-                        sts128(q0 + (r < half ? 0 : S::QGROUP) + (c >> 3) * S::ROWS * 128 + r1 * 128 + (((c & 7) ^ (r1 & 7)) << 4), x[i]);
+                        sts128(q0 + (r < half ? 0 : S::QGROUP) + (c >> 3) * S::QROWS * 128 + r1 * 128 + (((c & 7) ^ (r1 & 7)) << 4), x[i]);
                         if (c == 0) qc[buf * RS + r] = kScale;
                     }
                 }
@@ -877,7 +906,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
         const uint32_t bar = kSoftBar + group;
         const int L = (warp & 3) * 32 + lane;
         const int e = L - (128 - D);  // element of the row; head_dim 64: lanes 64 .. 127
-        const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16) + group * 4 * N;
+        const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16) + group * S::GCOLS;
         const float kScale = rsqrtf((float)D) * 1.4426950408889634f;
         bool fail = false;
         int g = 0;
@@ -900,7 +929,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
             for (int c0 = 0; c0 < RW; c0 += 8) {
                 if (c0 >= nr) break;
                 float o[8];
-                load_terms<FP8, RW>(trow + (2 + (k & 1)) * N + c0, o);
+                load_out<FP8, RW>(trow + 2 * NS + (k & 1) * NO + c0, o);
 #pragma unroll
                 for (int i = 0; i < 8 && i < RW; ++i) {
                     const int r = c0 + i;
@@ -952,7 +981,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
             const int limit = info[buf].limit, least = info[buf].least, more = info[buf].more;
             const float *qcb = qc + buf * RS + R0;
             const int *bnd = bound + buf * RS + R0;
-            const uint32_t o_col = trow + (2 + (k & 1)) * N;
+            const uint32_t o_col = trow + 2 * NS + (k & 1) * NO;
             // Sums of weights, and references.
             float *const ms = mref + (k & 1) * GS;
             float l[RW], mr[RW];
@@ -983,7 +1012,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                 for (int c0 = 0; c0 < RW; c0 += CH) {
                     if (c0 >= nr) break;
                     float x[CH];
-                    load_terms<FP8, RW>(trow + b * N + c0, x);
+                    load_logits<FP8, RW>(trow + b * NS + c0, x);
 #pragma unroll
                     for (int i = 0; i < CH && i < RW; ++i) {
                         if (i % GR == 0 && c0 + i >= nr) break;
@@ -1068,13 +1097,13 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                         }
                         if (any && t > t0) {
                             float o[8];
-                            if constexpr (FP8 && RW >= 8) {
+                            if constexpr (RW >= 8) {
                                 float o2[8];
                                 tmem_ld_pair(o_col + c0, o_col + RW + c0, o, o2);
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) o[i] *= f[i], o2[i] *= f[i];
                                 tmem_st8(o_col + RW + c0, o2);
-                            } else {  // with fewer than 8 rows both terms are in these columns
+                            } else {  // with fewer than 8 rows all terms are in these columns
                                 tmem_ld8(o_col + c0, o);
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) o[i] *= f[i % W];
@@ -1088,7 +1117,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                 // Row n of the weights' operand, this key's element: 128 n bytes on, with the 16-byte column of a row turned by
                 // its number in 8 (the swizzle).
                 const uint32_t key_at = S::OFF_P + b * S::PBUF + group * S::PGROUP +
-                                        (FP8 ? (uint32_t)L : (uint32_t)(L >> 6) * S::ROWS * 128 + (L & 63) * 2);
+                                        (FP8 ? (uint32_t)L : (uint32_t)(L >> 6) * S::PROWS * 128 + (L & 63) * 2);
                 auto at = [&](int n) { return smem + (key_at ^ ((n & 7) << 4)) + n * 128; };
                 const float hold = sv * (float)(1 << S::HELD);
 #pragma unroll
@@ -1107,9 +1136,13 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                         *at(RW + r) = (unsigned char)c;
                         *at(RW + r + 1) = (unsigned char)(c >> 8);
                     } else {
+                        // w = t1 + t2, to 2^-16 of it
                         const __nv_bfloat162 h = __floats2bfloat162_rn(w0, w1);
+                        const __nv_bfloat162 c = __floats2bfloat162_rn(w0 - __low2float(h), w1 - __high2float(h));
                         *reinterpret_cast<__nv_bfloat16 *>(at(r)) = h.x;
                         *reinterpret_cast<__nv_bfloat16 *>(at(r + 1)) = h.y;
+                        *reinterpret_cast<__nv_bfloat16 *>(at(RW + r)) = c.x;
+                        *reinterpret_cast<__nv_bfloat16 *>(at(RW + r + 1)) = c.y;
                     }
                 }
                 if ((t + 1) * kTile > limit) {
@@ -1184,6 +1217,12 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
 // 4000 to 8196 keys x 20 to 64 rows, E4M3: 138 us, 0.44 of the copy bandwidth.
 // The two halves taking whole tiles in turn, each thread a row of 128 keys,
 // took 193 us there when this form took 134.
+//
+// bf16: a weight is rounded to one bf16 number, 2^-8 of it, as the values beside
+// it and the result are.  A second term costs what the tensor cores have no room
+// for: 2 x 4096 tokens, 32 heads over 8 of 128, 277 us with one and 358 with
+// two; 4096 tokens over 20480 keys 854 and 1161; 2 x 2048 tokens, 24 heads over 8
+// of 64, 72 and 78.
 //
 // E4M3: the queries' two terms are accumulated into the same S, the second
 // unscaled (to 2^-19 of the row's largest element).  A weight is rounded to 9
