@@ -15,13 +15,17 @@
 // as the K-major, V as the M-major operand): no key or value passes through
 // a register, and a handful of rows fills the 128-row tensor-core tile.
 //
-// An E4M3 cache is multiplied as E4M3.  The other operand is split into two
-// E4M3 numbers, x = t1 + t2 / 16, in columns of their own (a tile has 16 at
-// the least): a bf16 query is the sum of two exactly (8 = 4 + 4 significant
-// bits) but for elements under 2^-22 of its row's largest; a weight is held
-// to 8 bits, or 2^-19 of the reference.  The scale of a page and head enters
-// the logit (K) and the weight (V); since a page's weight times its scale is
-// what is rounded, m refers to logit + log2(V scale).
+// An E4M3 cache is multiplied as E4M3, the other operand split into numbers of
+// 8 bits in columns of their own (a tile has 16 at the least).  A bf16 query is
+// t1 + t2 / 16 of two E4M3 numbers, exactly (8 = 4 + 4 significant bits) but for
+// elements under 2^-22 of its row's largest.  A weight is the sum of three E5M2
+// numbers: 9 bits, down to 2^-28 of the reference, so that thousands of keys
+// beside a dominant one keep theirs (two E4M3 numbers, 8 bits down to 2^-18, lost
+// 90 % of an output that 8200 keys of e^-13 to e^-15 made up, and took 55.9 us
+// instead of 56.2 for 96 sequences of 65 to 640 keys, 85.9 instead of 88.5 for 32 x
+// 4000 keys x 32 rows).  The scale of a
+// page and head enters the logit (K) and the weight (V); since a page's weight
+// times its scale is what is rounded, m refers to logit + log2(V scale).
 //
 // Over a bf16 cache a weight is the sum of two bf16 numbers, to 2^-16 of it, in
 // columns of their own likewise.  The second costs nothing where the cache's
@@ -107,9 +111,9 @@ struct Shape {
     static constexpr int SOFT = 1 + GROUPS, QUERY = 1 + 5 * GROUPS;  // first softmax warp, query warp
     static constexpr int QD = RB == 2 ? 3 : 2;             // items whose queries are in shared memory
     static constexpr int TERMS = FP8 ? 2 : 1;    // numbers that a query's element is split into
-    static constexpr int WTERMS = 2;             // and a weight
+    static constexpr int WTERMS = FP8 ? 3 : 2;   // and a weight
     static constexpr int NS = TERMS * RW < 16 ? 16 : TERMS * RW;    // columns of a group's S^T
-    static constexpr int NO = WTERMS * RW < 16 ? 16 : WTERMS * RW;  // and O^T
+    static constexpr int NO = (WTERMS * RW + 15) / 16 * 16;         // and O^T
     // A bf16 tile of head_dim 128 goes through the ring of slots as its K part
     // and its V part, others whole.  A part is C columns of 128 bytes; 8 keys of
     // column 0, the same keys of column 1, .., then the next 8 keys.
@@ -130,9 +134,9 @@ struct Shape {
     static constexpr int TCOLS = GCOLS * GROUPS;
     static constexpr int TMEM = TCOLS <= 64 ? 64 : TCOLS <= 128 ? 128 : TCOLS <= 256 ? 256 : 512;
     // log2 of how far a weight may pass 1 before the references move, and of
-    // the factor that weights are held with (E4M3 reaches 448).
+    // the factor that weights are held with (fp16 reaches 2^16, E5M2 almost).
     static constexpr int SLACK = FP8 ? 3 : 8;
-    static constexpr int HELD = FP8 ? 8 - SLACK : 0;
+    static constexpr int HELD = FP8 ? 15 - SLACK : 0;
     static constexpr int PIECE = RB * (D + 2);  // floats of a published piece: O, m, l
     // Few rows leave the tensor cores idle while a tile's weights are made:
     // other CTAs of the SM fill in.  In bf16 a block of 16 takes one CTA with
@@ -361,16 +365,6 @@ __device__ __forceinline__ void lane_reduce(float (&v)[R], int lane, Op op)
     for (int h = R; h < 32; h <<= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], h));
 }
 
-__device__ __forceinline__ uint32_t e4m3_of_half2(__half2 h)
-{
-    return __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw *>(&h), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ __half2 half2_of_e4m3(uint32_t c)
-{
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3);
-    return *reinterpret_cast<const __half2 *>(&h);
-}
-
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -429,18 +423,39 @@ __device__ __forceinline__ void load_logits(uint32_t col, float (&x)[n])
 template <bool FP8, int RW>
 __device__ __forceinline__ void load_out(uint32_t col, float (&x)[8])
 {
-    constexpr float second = FP8 ? 0.0625f : 1.f;
-    if constexpr (RW < 8) {
+    if constexpr (RW < 8) {  // all terms lie in 8 columns
         tmem_ld8(col, x);
 #pragma unroll
-        for (int i = 0; i < RW; ++i) x[i] = fmaf(x[RW + i], second, x[i]);
+        for (int i = 0; i < RW; ++i) x[i] += FP8 ? x[RW + i] + x[2 * RW + i] : x[RW + i];
     } else {
         float y[8];
         tmem_ld_pair(col, col + RW, x, y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = fmaf(y[i], second, x[i]);
+        for (int i = 0; i < 8; ++i) x[i] += y[i];
+        if constexpr (FP8) {
+            tmem_ld8(col + 2 * RW, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] += y[i];
+        }
     }
 }
+
+// Two fp16 weights, rounded to 9 bits, as three E5M2 numbers each, in the upper
+// bytes of the fp16 halves: 3 bits from the top of what is left, the
+// differences exact.  What is below 2^-16 is cut off.
+__device__ __forceinline__ void cut_weights(__half2 w, uint32_t (&t)[3])
+{
+    const uint32_t u = (*reinterpret_cast<const uint32_t *>(&w) + 0x00020002u) & 0xfffcfffcu;
+    t[0] = u & 0xff00ff00u;
+    const uint32_t rest = half2_less(u, t[0]);
+    t[1] = rest & 0xff00ff00u;
+    t[2] = half2_less(rest, t[1]);
+}
+
+// Half a step of what the cut leaves, 2^-16: numbers below 2^-6 are rounded by
+// it instead of cut off, so that thousands of them do not lose the same part.
+// Above, it moves a number by 2^-11 of it at the most.
+constexpr float kHalfCut = 0x1p-17f;
 
 // The producer warp of a kernel of shape S.  Returns the copies it issued.
 template <typename S, bool FP8, int RB>
@@ -745,7 +760,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
         // issues; a lone lane in a branch would make the compiler move every
         // operand to the uniform registers inside it, MMA by MMA.
         constexpr uint32_t id_s = FP8 ? idesc_e4m3_f32(128, NS) : idesc_bf16_f32(128, NS);
-        constexpr uint32_t id_o = (FP8 ? idesc_e4m3_f32(128, NO) : idesc_bf16_f32(128, NO)) | kIdescAMMajor;
+        constexpr uint32_t id_o = (FP8 ? idesc_e4m3_f32(128, NO) | kIdescBE5M2 : idesc_bf16_f32(128, NO)) | kIdescAMMajor;
         const bool leader = elect_one();
         const uint32_t s_col = tmem + group * S::GCOLS, o_col = s_col + 2 * NS;
         int g = 0, taken = 0, slot_before = 0;
@@ -1102,13 +1117,20 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                                 tmem_ld_pair(o_col + c0, o_col + RW + c0, o, o2);
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) o[i] *= f[i], o2[i] *= f[i];
+                                tmem_st8(o_col + c0, o);
                                 tmem_st8(o_col + RW + c0, o2);
+                                if constexpr (FP8) {
+                                    tmem_ld8(o_col + 2 * RW + c0, o);
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) o[i] *= f[i];
+                                    tmem_st8(o_col + 2 * RW + c0, o);
+                                }
                             } else {  // with fewer than 8 rows all terms are in these columns
                                 tmem_ld8(o_col + c0, o);
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) o[i] *= f[i % W];
+                                tmem_st8(o_col + c0, o);
                             }
-                            tmem_st8(o_col + c0, o);
                         }
                     }
                 }
@@ -1127,14 +1149,13 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                     l[r] += w0;
                     l[r + 1] += w1;
                     if (FP8) {
-                        // w = t1 + t2 / 16; fp16 holds w to 11 bits, so the difference is exact
-                        const __half2 h = __floats2half2_rn(w0 * hold, w1 * hold);
-                        const uint32_t a = e4m3_of_half2(h);
-                        const uint32_t c = e4m3_of_half2(__hmul2(__hsub2(h, half2_of_e4m3(a)), __float2half2_rn(16.f)));
-                        *at(r) = (unsigned char)a;
-                        *at(r + 1) = (unsigned char)(a >> 8);
-                        *at(RW + r) = (unsigned char)c;
-                        *at(RW + r + 1) = (unsigned char)(c >> 8);
+                        uint32_t terms[3];
+                        cut_weights(__floats2half2_rn(fmaf(w0, hold, kHalfCut), fmaf(w1, hold, kHalfCut)), terms);
+#pragma unroll
+                        for (int i = 0; i < 3; ++i) {
+                            *at(i * RW + r) = (unsigned char)(terms[i] >> 8);
+                            *at(i * RW + r + 1) = (unsigned char)(terms[i] >> 24);
+                        }
                     } else {
                         // w = t1 + t2, to 2^-16 of it
                         const __nv_bfloat162 h = __floats2bfloat162_rn(w0, w1);
@@ -1225,12 +1246,11 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
 // of 64, 72 and 78.
 //
 // E4M3: the queries' two terms are accumulated into the same S, the second
-// unscaled (to 2^-19 of the row's largest element).  A weight is rounded to 9
-// bits and cut into three E5M2 numbers of 3 bits each, which are the upper
-// bytes of fp16 numbers: no conversion instruction (conversions to E4M3 and
-// back took as long as the exponentials), no scale between the terms, one
-// accumulator.  Off by at most 2^-9 of the weight plus 2^-25 of the reference; a
-// NaN becomes a zero there, and the row is NaN by its sum.
+// unscaled (to 2^-19 of the row's largest element).  A weight is cut as above,
+// without a conversion instruction (conversions to E4M3 and back took as long as
+// the exponentials) or a scale between the terms: one accumulator.  Off by at
+// most 2^-9 of the weight plus 2^-26 of the reference; a NaN becomes a zero
+// there, and the row is NaN by its sum.
 template <bool FP8, int D>
 struct Rows {
     static constexpr int RB = 128;
@@ -1572,22 +1592,15 @@ __global__ void __launch_bounds__(Rows<FP8, D>::THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 64; j += 4) {
                         const float hold = sv[j / 16] * (float)(1 << S::HELD);
-                        uint32_t a[2], d[2], e[2];
+                        uint32_t a[3], d[3];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const float w0 = ex2(y[j + 2 * i]), w1 = ex2(y[j + 2 * i + 1]);
                             l += w0 + w1;
-                            const __half2 w = __floats2half2_rn(w0 * hold, w1 * hold);
-                            // to 9 bits; then 3 bits a term from the top, the differences exact
-                            const uint32_t u = (*reinterpret_cast<const uint32_t *>(&w) + 0x00020002u) & 0xfffcfffcu;
-                            a[i] = u & 0xff00ff00u;
-                            const uint32_t rest = half2_less(u, a[i]);
-                            d[i] = rest & 0xff00ff00u;
-                            e[i] = half2_less(rest, d[i]);
+                            cut_weights(__floats2half2_rn(fmaf(w0, hold, kHalfCut), fmaf(w1, hold, kHalfCut)), i == 0 ? a : d);
                         }
-                        terms[0][j / 4] = __uint_as_float(__byte_perm(a[0], a[1], 0x7531));
-                        terms[1][j / 4] = __uint_as_float(__byte_perm(d[0], d[1], 0x7531));
-                        terms[2][j / 4] = __uint_as_float(__byte_perm(e[0], e[1], 0x7531));
+#pragma unroll
+                        for (int term = 0; term < 3; ++term) terms[term][j / 4] = __uint_as_float(__byte_perm(a[term], d[term], 0x7531));
                     }
 #pragma unroll
                     for (int term = 0; term < 3; ++term) tmem_st16(s_col + 16 * term, terms[term]);

@@ -136,6 +136,7 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N)
 constexpr uint32_t kIdescAMMajor = 1u << 15;
 constexpr uint32_t kIdescBNMajor = 1u << 16;  // and B N-major
 constexpr uint32_t kIdescAE5M2 = 1u << 7;     // and, in kind::f8f6f4, A of E5M2
+constexpr uint32_t kIdescBE5M2 = 1u << 10;    // or B
 
 // D[tmem] (+)= A[adesc] * B[bdesc]^T for one K = 32 slice of E4M3; issued by
 // one thread.  accumulate == 0 overwrites D.

@@ -123,10 +123,11 @@ int dsa_paged_append(dsa_paged h, int n_seqs, int n_tokens, const int32_t *cu, c
  * sequence, rows that a NaN or infinity in a later new token's V meets.
  * Products are exact, sums and softmax statistics fp32.  For DSA_FP8_E4M3 an
  * element of q enters the first product to 8 significant bits and 2^-19 of its
- * row's largest.  The weights enter the second product with 8 significant bits
- * (for DSA_FP8_E4M3 also to 2^-19 of the row's largest only; for DSA_BF16 with
- * 16 bits where a sequence has at most 16 rows, new tokens x grouped query
- * heads), and the result is rounded to bf16 once.
+ * row's largest.  The weights enter the second product with 16 significant
+ * bits (DSA_BF16, where a sequence has at most 16 rows, new tokens x grouped
+ * query heads), 8 (DSA_BF16 with more rows) or 9 (DSA_FP8_E4M3: also down to
+ * 2^-26 of the row's largest product of a weight and its page's V scale, or less,
+ * rounded), and the result is rounded to bf16 once.
  * Deterministic for given arguments: pieces of one row are joined in the
  * order of their keys.
  * n_tokens == 0 or n_seqs == 0 is allowed.  Asynchronous on `stream`; a
