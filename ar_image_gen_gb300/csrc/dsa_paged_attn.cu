@@ -588,12 +588,15 @@ __device__ __forceinline__ void join_row(const float *work, int piece, int cf, i
     for (int v = 0; v < V; v += 2) dst[v / 2] = __floats2bfloat162_rn(o[v] * inv, o[v + 1] * inv);
 }
 
-// 8 elements of a query row as two E4M3 numbers each, (t1 + t2 / second)
-// times the returned scale 2^e, the smallest with every element of the row at
-// most 448 2^e; the row's other elements are in the TR - 1 lanes beside.  A
-// row with an infinity or NaN has the scale NaN.
-template <int TR>
-__device__ __forceinline__ float split_query(const uint4 &x, float second, uint32_t (&a)[4], uint32_t (&b)[4])
+// 8 elements of a query row as two numbers each, E4M3 and then E4M3 of 16 times
+// the rest, or (`plain`) E5M2 of the rest: 3 bits hold it, 8 bits less 4 rounded,
+// exactly where the first has its 4.  x = (t1 + t2 / 16 or t1 + t2) times the
+// returned scale 2^e, the smallest with every element of the row at most
+// 448 2^e; below 2^-6 of it the rest loses no more than 2^-14, 2^-21 of the row's
+// largest.  The row's other elements are in the TR - 1 lanes beside.  A row with
+// an infinity or NaN has the scale NaN.
+template <int TR, bool plain>
+__device__ __forceinline__ float split_query(const uint4 &x, uint32_t (&a)[4], uint32_t (&b)[4])
 {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     float v[8], top = 0.f;
@@ -615,7 +618,10 @@ __device__ __forceinline__ float split_query(const uint4 &x, float second, uint3
         const float y0 = v[2 * j] * inv, y1 = v[2 * j + 1] * inv;
         a[j] = e4m3_pair(y0, y1);
         const float2 t = e4m3_values(a[j]);
-        b[j] = e4m3_pair((y0 - t.x) * second, (y1 - t.y) * second);
+        if (plain)
+            b[j] = __nv_cvt_float2_to_fp8x2(make_float2(y0 - t.x, y1 - t.y), __NV_SATFINITE, __NV_E5M2);
+        else
+            b[j] = e4m3_pair((y0 - t.x) * 16.f, (y1 - t.y) * 16.f);
     }
     return top < INFINITY ? __uint_as_float((uint32_t)(127 + e) << 23) : NAN;
 }
@@ -873,7 +879,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                     if (r0 + i * kPass >= nr) break;
                     if (FP8) {
                         uint32_t a[4], b[4];
-                        const float scale = split_query<TR>(x[i], 16.f, a, b);
+                        const float scale = split_query<TR, false>(x[i], a, b);
                         if (r < nr) {
                             const int r1 = r < half ? r : r - half, r2 = S::RW + r1;
                             const uint32_t to = q0 + (r < half ? 0 : S::QGROUP) + (c & 1) * 8;
@@ -1246,7 +1252,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
 // of 64, 72 and 78.
 //
 // E4M3: the queries' two terms are accumulated into the same S, the second
-// unscaled (to 2^-19 of the row's largest element).  A weight is cut as above,
+// unscaled and so E5M2, for its range.  A weight is cut as above,
 // without a conversion instruction (conversions to E4M3 and back took as long as
 // the exponentials) or a scale between the terms: one accumulator.  Off by at
 // most 2^-9 of the weight plus 2^-26 of the reference; a NaN becomes a zero
@@ -1415,7 +1421,7 @@ __global__ void __launch_bounds__(Rows<FP8, D>::THREADS, 1)
                         const uint64_t q = qd + (uint64_t)((s / kSteps * S::QTERM + i / 4 * kBox + i % 4 * 32) / 16);
                         const uint64_t key = kd + (uint64_t)((i / 4 * 1024 + i % 4 * 32) / 16);
                         if (FP8)
-                            umma_e4m3(tmem + (g & 1) * 128, q, key, id_s, s > 0);
+                            umma_e4m3(tmem + (g & 1) * 128, q, key, s < kSteps ? id_s : id_s | kIdescAE5M2, s > 0);
                         else
                             umma_bf16(tmem + (g & 1) * 128, q, key, id_s, s > 0);
                     }
@@ -1477,7 +1483,7 @@ __global__ void __launch_bounds__(Rows<FP8, D>::THREADS, 1)
                     const int r = r0 + i * kPass + lane / TR;
                     if (r0 + i * kPass >= nr) break;
                     uint32_t a[4], b[4];
-                    const float scale = split_query<TR>(x[i], 1.f, a, b);
+                    const float scale = split_query<TR, true>(x[i], a, b);
                     const uint32_t to = q0 + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
                     sts64(to, a[0] | a[1] << 16, a[2] | a[3] << 16);
                     sts64(to + S::QTERM, b[0] | b[1] << 16, b[2] | b[3] << 16);

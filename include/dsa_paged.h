@@ -122,7 +122,7 @@ int dsa_paged_append(dsa_paged h, int n_seqs, int n_tokens, const int32_t *cu, c
  * row whose logits hold a NaN is NaN; so are, among the new tokens of the
  * sequence, rows that a NaN or infinity in a later new token's V meets.
  * Products are exact, sums and softmax statistics fp32.  For DSA_FP8_E4M3 an
- * element of q enters the first product to 8 significant bits and 2^-19 of its
+ * element of q enters the first product to 8 significant bits and 2^-21 of its
  * row's largest.  The weights enter the second product with 16 significant
  * bits (DSA_BF16, where a sequence has at most 16 rows, new tokens x grouped
  * query heads), 8 (DSA_BF16 with more rows) or 9 (DSA_FP8_E4M3: also down to

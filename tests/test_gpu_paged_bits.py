@@ -7,9 +7,10 @@ it; with more than 16 rows of a sequence and KV head one number: 2^-8.  E4M3
 caches: a weight is rounded to fp16 and to 9 bits, half a step of which is
 2^-9, and moved by half a step of the cut, 2^-11 at the most: 2^-9 + 2^-10 with
 fp16's own; it keeps half a step of 2^-28 (2^-25 with more than 32 rows) of the
-reference that weight x V scale refers to, twice that of the largest weight times the
-largest |v| where the pages' scales are alike.  fp32 logits, exponentials and sums: 2^-15 for logits up to some
-tens.  The result is rounded once: 2^-8.
+reference that weight x V scale refers to, twice that of the largest weight
+times the largest |v| where the pages' scales are alike.  An element of q over
+an E4M3 cache is held to 2^-21 of its row's largest.  fp32 logits, exponentials
+and sums: 2^-15 for logits up to some tens.  The result is rounded once: 2^-8.
 """
 import numpy as np
 import pytest
@@ -108,3 +109,18 @@ def test_many_small_weights_beside_a_large_one(dsa, kv, d, Hq, Hk, new):
     assert cache.sync_status() == 0
     for got in out.reshape(S, new, Hq, d).unique(dim=0):
         compare(c, got, stored(cache, c), rows=new * Hq // Hk)
+
+
+@pytest.mark.parametrize("Hq,Hk,new", BLOCKS[:5])
+def test_queries_with_an_outlier(dsa, Hq, Hk, new):
+    """Elements 2^-12 of their row's largest, alike, over keys of one sign: their errors add up in the logit."""
+    d = 64
+    n = max(new, 4)
+    c = Case("fp8e4m3", Hq, Hk, d, 16, [n], [new], seed=5)
+    c.q[:] = 49 / 1024
+    c.q[:, :, 0] = 240
+    k = (torch.arange(n) % 4 * 4 / 3)[:, None, None].expand(n, Hk, d).clone()
+    k[:, :, 0] = 0
+    v = torch.randn((n, Hk, d), generator=torch.Generator().manual_seed(1))
+    # 63 elements, each off by 2^-21 of 240, with keys of 4
+    attend_and_check(c, k=k.to(torch.bfloat16), v=v.to(torch.bfloat16), logits=63 * 240 * 2.0 ** -21 * 4 / 8)
