@@ -58,12 +58,13 @@ __device__ __forceinline__ int exponent_v(float a)
     return min(max(e, kEMin), kEMax);
 }
 
-// The smallest e with a <= (448 * 2^e)^2 (a = 1.53125 * 2^17 at e = 0).
+// The smallest e with a <= (448 * 2^e)^2 (a = 1.53125 * 2^17 at e = 0).  Below
+// 2^-126 a mantissa has no leading one; both candidates are known there.
 __device__ __forceinline__ int exponent_k(float a)
 {
     const uint32_t u = __float_as_uint(a);
     const int e = (int)(u >> 23) - 127 - 17 + ((u & 0x7fffffu) > 0x440000u);
-    return min(max((e + 1) >> 1, kEMin), kEMax);
+    return a < 0x1p-126f ? kEMin + (a > 0x1.88p-127f) : min(max((e + 1) >> 1, kEMin), kEMax);
 }
 
 __device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
@@ -145,15 +146,15 @@ __device__ bool find_chunk(const Batch &b, int chunk_log2, int c, Chunk *found, 
 }
 
 // The largest value of a raw row half-pair that sets a scale: |v|, or for keys
-// the squared norm of a rotated pair (square of another element).
-__device__ __forceinline__ float reach8(const uint4 &lo, const uint4 &hi, bool value, int j0, int pairs)
+// the squared norm of a rotated pair (square of another element) times unit^2.
+__device__ __forceinline__ float reach8(const uint4 &lo, const uint4 &hi, bool value, int j0, int pairs, float unit)
 {
     float a[8], b[8], top = 0.f;
     unpack8(lo, a);
     unpack8(hi, b);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float x = finite_or_0(a[i]), z = finite_or_0(b[i]);
+        const float x = finite_or_0(a[i]) * unit, z = finite_or_0(b[i]) * unit;
         if (value)
             top = fmaxf(top, fmaxf(fabsf(x), fabsf(z)));
         else if (j0 + i < pairs)
@@ -252,21 +253,32 @@ __global__ void __launch_bounds__(kAppendThreads, FP8 ? 3 : 4) append_kernel(con
             const bool value = mine & 1;
             float *const at = p.scales + (size_t)page * 2 * p.Hk + mine;
             const float old = mine < u1 && slot0 > 0 ? *at : 0.f;
-            float top = 0.f;
-            if (kept) {
-                if (u != u0 + warp * per) fetch(mine);
+            if (kept && u != u0 + warp * per) fetch(mine);
+            auto search = [&](float unit) {
+                float top = 0.f;
+                if (kept) {
 #pragma unroll
-                for (int i = 0; i < kKeep; ++i)
-                    if (mine < u1 && sub % side + i * side < m) top = fmaxf(top, reach8(lo[i], hi[i], value, j0, pairs));
-            } else if (mine < u1) {
+                    for (int i = 0; i < kKeep; ++i)
+                        if (mine < u1 && sub % side + i * side < m) top = fmaxf(top, reach8(lo[i], hi[i], value, j0, pairs, unit));
+                } else if (mine < u1) {
 #pragma unroll 4
-                for (int t = sub % side; t < m; t += side)
-                    top = fmaxf(top, reach8(raw(given(mine, t)), raw(given(mine, t) + D / 2), value, j0, pairs));
+                    for (int t = sub % side; t < m; t += side)
+                        top = fmaxf(top, reach8(raw(given(mine, t)), raw(given(mine, t) + D / 2), value, j0, pairs, unit));
+                }
+                for (int o = 1; o < L * side; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                return top;
+            };
+            const float top = search(1.f);
+            int e = value ? exponent_v(top) : exponent_k(top);
+            // A norm from 2^64 on: its square has left fp32.
+            const bool beyond = !value && top == INFINITY;
+            if (__any_sync(0xffffffffu, beyond)) {
+                const int far = exponent_k(search(0x1p-66f)) + 66;
+                if (beyond) e = min(far, kEMax);
             }
-            for (int o = 1; o < L * side; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             __syncwarp();  // every lane has read the old scale
             if (mine < u1) {
-                float scale = two_to(value ? exponent_v(top) : exponent_k(top));
+                float scale = two_to(e);
                 if (old >= scale) {
                     scale = old;
                 } else if (slot0 > 0) {

@@ -89,8 +89,8 @@ int dsa_paged_destroy(dsa_paged h);
  * with e in [-72, 120]: a floating-point code loses nothing to it, and codes
  * move to a larger one by their exponents.  e is the smallest for which the
  * largest finite |v| of the page's new tokens is at most 448 * 2^e; for K the
- * norm of a rotated pair (fp32, which the rotation leaves alone) takes the
- * place of |v|, so a scale depends on neither position nor rounding.  A
+ * norm of a rotated pair (which the rotation leaves alone; its square rounded to
+ * the 24 bits of fp32, of any exponent) takes the place of |v|, so a scale depends on neither position nor rounding.  A
  * token in slot 0 starts the page's scale anew; later tokens keep the larger
  * of the old and the new, and where it grows the codes of the earlier tokens
  * become the codes nearest to code * old / new (exact but for subnormals).

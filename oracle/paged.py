@@ -62,12 +62,13 @@ def _smallest(a):
 
 def k_reach(k, rotated):
     """Per row the largest norm of a rotated pair or magnitude of another element (finite ones), the
-    squared norm rounded to fp32 as the definition says."""
+    squared norm rounded to the 24 bits of fp32 (not to its range) as the definition says."""
     k = np.where(np.isfinite(k), k, 0.0).astype(np.float64)
     h = k.shape[-1] // 2
     sq = (k ** 2)
     both = np.concatenate([sq[..., :rotated] + sq[..., h:h + rotated], sq[..., rotated:h], sq[..., h + rotated:]], -1)
-    return np.sqrt(both.max(-1).astype(np.float32).astype(np.float64))
+    m, e = np.frexp(both.max(-1))
+    return np.sqrt(np.ldexp(m.astype(np.float32).astype(np.float64), e))
 
 
 def v_reach(v):
