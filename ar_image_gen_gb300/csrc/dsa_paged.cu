@@ -35,7 +35,6 @@ using namespace dsa;
 constexpr int kAppendThreads = 256;
 constexpr int kRun = 16;        // tokens whose sines are in shared memory at once
 constexpr int kMaxParts = 256;  // (head, K / V) pairs whose scales one CTA holds
-constexpr int kEMin = -72, kEMax = 120;
 
 struct AppendParams {
     Batch b;

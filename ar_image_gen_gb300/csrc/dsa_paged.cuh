@@ -18,6 +18,8 @@ enum : int { ST_TIMEOUT = 1, ST_CHECK = 2 };
 constexpr int kMaxGrid = 1024;  // CTAs of the attention at most
 constexpr int kCounters = 2 * kMaxGrid;  // one per CTA and softmax group
 
+constexpr int kEMin = -72, kEMax = 120;  // exponents of the append's scales
+
 constexpr int kMaxLen = 0x7fffff00;  // tokens of a sequence at most: positions rounded up to a tile stay in 31 bits
 
 // The batch of a call (device memory) and what bounds it.

@@ -419,6 +419,15 @@ __device__ __forceinline__ void load_logits(uint32_t col, float (&x)[n])
     }
 }
 
+// ceil(log2) of a page's V scale, from the append's smallest on: a scale of 0 (a
+// page that is not there is read as zeros, its scales too) must not draw the
+// reference so far down that the weights overflow.
+__device__ __forceinline__ float scale_log2(float sv)
+{
+    const uint32_t u = __float_as_uint(sv) & 0x7fffffffu;
+    return (float)max((int)(u >> 23) - 127 + ((u & 0x7fffffu) != 0), kEMin);
+}
+
 // 8 columns of O^T at `col`, the terms of their weights joined.
 template <bool FP8, int RW>
 __device__ __forceinline__ void load_out(uint32_t col, float (&x)[8])
@@ -1021,8 +1030,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                                                                         (L >> p.b.page_log2) * 8);
                     sk = sc.x;
                     sv = sc.y;
-                    const uint32_t u = __float_as_uint(sv) & 0x7fffffffu;  // ceil(log2 sv)
-                    ev = (float)((int)(u >> 23) - 127 + ((u & 0x7fffffu) != 0));
+                    ev = scale_log2(sv);
                 }
                 tc_fence_after();
                 const bool whole = (t + 1) * kTile <= least;  // no row of the block is masked
@@ -1545,8 +1553,7 @@ __global__ void __launch_bounds__(Rows<FP8, D>::THREADS, 1)
                                                                             ((half * 64 + 16 * j) >> p.b.page_log2) * 8);
                         sk[j] = sc.x;
                         sv[j] = sc.y;
-                        const uint32_t u = __float_as_uint(sc.y) & 0x7fffffffu;  // ceil(log2 sv)
-                        ev[j] = (float)((int)(u >> 23) - 127 + ((u & 0x7fffffu) != 0));
+                        ev[j] = scale_log2(sc.y);
                     }
                 }
                 // y: logits (log2) less the reference so far; masked ones are -inf.

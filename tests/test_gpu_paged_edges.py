@@ -1,10 +1,13 @@
 """The paged cache at the ends of its range, against the 64-bit oracle: keys
-of any size.  Tolerances: tests/test_gpu_paged.py.
+of any size, pages that are missing for whole tiles.  Tolerances:
+tests/test_gpu_paged.py, and tests/paged_case.py for the attention.
 """
+import numpy as np
 import pytest
 import torch
 
-from tests.paged_case import Case
+from oracle import paged as ref
+from tests.paged_case import Case, check_attend
 from tests.test_gpu_paged import append_and_check
 
 pytestmark = pytest.mark.gpu
@@ -18,6 +21,15 @@ def dsa():
     build()
     from ar_image_gen_gb300 import dsa as mod
     return mod
+
+
+def attended(c, kv, values, table=None, status=0, max_new=None):
+    """Attends the case over what kv holds and compares with the oracle over `values`."""
+    cu, lens, dev_table = c.batch()
+    out = torch.empty_like(c.q, device="cuda")
+    kv.attend(c.q.cuda(), cu, lens, dev_table, out, max_new=max_new or int(max(c.new)))
+    assert kv.sync_status() == status
+    check_attend(out, ref.attend(c.q.double().numpy(), values, c.cu, c.lens, c.table if table is None else table), c.kv)
 
 
 # ---- the K scale -----------------------------------------------------------
@@ -46,3 +58,36 @@ def test_a_scale_grows_to_a_large_key(dsa):
     c = Case("fp8e4m3", 1, 1, 64, 16, [9, 12], [2, 1], seed=8)
     c.k[0], c.k[1], c.k[2] = 1e25, 1e21, 3e37
     append_and_check(dsa, c, ())
+
+
+# ---- pages that are missing, and scales of 0 --------------------------------
+
+@pytest.mark.parametrize("kv_type,zero", [("bf16", False), ("fp8e4m3", False), ("fp8e4m3", True)])
+@pytest.mark.parametrize("lens,new,gone", [
+    ([700], [1], 16), ([700], [3], 24), ([700], [12], 24), ([700], [40], 16), ([1500, 400], [40, 1], 24), ([20000], [1], 900),
+    ([20000], [40], 900), ([20000], [1], 1248),
+])
+def test_tiles_of_missing_pages(dsa, kv_type, zero, lens, new, gone):
+    """A dropped prefix: the first `gone` pages are no pages of the pool (or have scales of 0), tiles of nothing else
+    among them; they hold zeros, whose weights count."""
+    c = Case(kv_type, 4, 2, 64, 16, lens, new, seed=2)
+    values = np.concatenate([c.values, np.zeros((1,) + c.values.shape[1:])])
+    table = c.table.copy()
+    for s in range(len(lens)):
+        m = min(gone, (lens[s] - new[s]) // 16 - 1)
+        table[s, :m] = c.n_pages
+        if zero:
+            c.scales[c.table[s, :m]] = 0
+        else:
+            c.table[s, :m] = -1
+    kv = c.cache()
+    cu, lens_d, t = c.batch()
+    kv.append(None, c.k.cuda(), c.v.cuda(), cu, lens_d, t)
+    assert kv.sync_status() == dsa.DSA_OK
+    n = c.n_pages
+    if kv_type == "bf16":
+        values[:n] = kv.pages.double().cpu().numpy()
+    else:
+        codes = kv.pages.contiguous().view(torch.uint8).cpu().numpy().reshape(c.codes.shape)
+        values[:n] = ref.e4m3_decode(codes) * kv.scales.double().cpu().numpy()[:, :, None, :, None]
+    attended(c, kv, values, table, dsa.DSA_OK if zero else dsa.DSA_ERR_DEVICE_CHECK)
