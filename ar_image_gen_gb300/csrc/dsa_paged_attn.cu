@@ -69,6 +69,13 @@ constexpr uint32_t kSoftBar = 1;  // named barrier of the first softmax group
 constexpr int kTile = 128;     // keys of a tile
 constexpr uint32_t kBox = kTile * 128;  // bytes of one 128-byte column of a tile
 constexpr float kNoMax = -1e30f;
+// Of an E4M3 cache the reference is log2 of the largest weight x V scale, less
+// this.  A row's sum adds up the weights themselves, 2^kLow over the V scale of
+// the page that set the reference: with scales of 2^-72 to 2^120 from 2^-102,
+// where a key that weighs 2^-24 of it is still a normal number, to 2^96, which
+// 2^31 keys do not carry out of fp32.  (From 0 instead, V of 1e36 lost the keys
+// under 2^-7 of the largest.)
+constexpr int kLow = 18;
 constexpr uint32_t kBarBytes = 320;
 constexpr int kScaleRing = 8;  // tiles whose page scales are in shared memory
 
@@ -136,7 +143,8 @@ struct Shape {
     // log2 of how far a weight may pass 1 before the references move, and of
     // the factor that weights are held with (fp16 reaches 2^16, E5M2 almost).
     static constexpr int SLACK = FP8 ? 3 : 8;
-    static constexpr int HELD = FP8 ? 15 - SLACK : 0;
+    static constexpr int LOW = FP8 ? kLow : 0;
+    static constexpr int HELD = FP8 ? 15 - SLACK - LOW : 0;
     static constexpr int PIECE = RB * (D + 2);  // floats of a published piece: O, m, l
     // Few rows leave the tensor cores idle while a tile's weights are made:
     // other CTAs of the SM fill in.  In bf16 a block of 16 takes one CTA with
@@ -324,6 +332,8 @@ __device__ __forceinline__ bool wait_poll(uint32_t bar, uint32_t parity, uint32_
     }
     return false;
 }
+
+__device__ __forceinline__ constexpr float power2(int e) { return e < 0 ? 1.f / (1 << -e) : (float)(1 << e); }
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -954,7 +964,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
             float *const piece = p.work + (size_t)(2 * blockIdx.x + ((int)blockIdx.x > cf)) * S::PIECE;
             // Lane r: the sum of row r.
             const float sum = lane < nr ? ls[lane] + ls[GS + lane] + ls[2 * GS + lane] + ls[3 * GS + lane] : 1.f;
-            const float scale = (pieces == 1 ? 1.f / sum : 1.f) * (1.f / (1 << S::HELD));
+            const float scale = (pieces == 1 ? 1.f / sum : 1.f) * power2(-S::HELD);
 #pragma unroll
             for (int c0 = 0; c0 < RW; c0 += 8) {
                 if (c0 >= nr) break;
@@ -1074,7 +1084,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                 }
                 const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 bool need = t == t0;
-                if (!need) need = named_bar_or(bar, kSoft, top > (float)S::SLACK - ev || fail);
+                if (!need) need = named_bar_or(bar, kSoft, top > (float)(S::SLACK + S::LOW) - ev || fail);
                 if (need) {
                     // New references: each row's largest logit + log2(V scale), where that has grown past the slack.
                     float v[RW];
@@ -1118,7 +1128,8 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                             if (i % GR == 0 && r >= nr) break;
                             // rows beyond the block never ask for more (and weigh nothing)
                             const float held = mr[r], old = t == t0 ? kNoMax : held;
-                            const float now = r >= nr ? -kNoMax : best[i] > old + (float)S::SLACK ? best[i] : old;
+                            const float low = best[i] - (float)S::LOW;
+                            const float now = r >= nr ? -kNoMax : low > old + (float)S::SLACK ? low : old;
                             if (now != old && r < nr) f[i] = ex2(old - now), any = true;
                             y[r] += held - now;
                             mr[r] = now;
@@ -1155,7 +1166,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                 const uint32_t key_at = S::OFF_P + b * S::PBUF + group * S::PGROUP +
                                         (FP8 ? (uint32_t)L : (uint32_t)(L >> 6) * S::PROWS * 128 + (L & 63) * 2);
                 auto at = [&](int n) { return smem + (key_at ^ ((n & 7) << 4)) + n * 128; };
-                const float hold = sv * (float)(1 << S::HELD);
+                const float hold = sv * power2(S::HELD);
 #pragma unroll
                 for (int r = 0; r < RW; r += 2) {
                     if (r % GR == 0 && r >= nr) break;
@@ -1286,7 +1297,7 @@ struct Rows {
     static constexpr int QBOXES = D * EB < 128 ? 1 : D * EB / 128;
     static constexpr uint32_t QTERM = QBOXES * kBox, QBUF = TERMS * QTERM;
     static constexpr int TMEM = 512;                         // S twice, O of the two halves
-    static constexpr int SLACK = FP8 ? 6 : 8, HELD = FP8 ? 15 - SLACK : 0;  // fp16 reaches 2^16
+    static constexpr int SLACK = FP8 ? 6 : 8, LOW = FP8 ? kLow : 0, HELD = FP8 ? 15 - SLACK - LOW : 0;  // fp16 reaches 2^16
     static constexpr int PIECE = RB * (D + 2);
     static constexpr uint32_t ROWF = (3 * QD + 4 + 4) * RB;  // qc, bound, orow [QD], refs [2][2], sums [2][2]
     static constexpr uint32_t FIXED = QD * QBUF + kBarBytes + kScaleRing * 64 + ROWF * 4 + QD * sizeof(Info) + 16 + 1024;
@@ -1576,10 +1587,10 @@ __global__ void __launch_bounds__(Rows<FP8, D>::THREADS, 1)
                     }
                     top = fmaxf(top, fmaxf(a, d) + ev[j]);
                 }
-                const bool grow = t == t0 || top > (float)S::SLACK;
+                const bool grow = t == t0 || top > (float)(S::SLACK + S::LOW);
                 if (__any_sync(0xffffffffu, grow)) {
                     // A new reference where the largest logit + log2(V scale) of the row has grown past the slack.
-                    const float d = !grow ? 0.f : t == t0 ? fmaxf(top, kNoMax) : top;
+                    const float d = !grow ? 0.f : (t == t0 ? fmaxf(top, kNoMax) : top) - (float)S::LOW;
                     m += d;
 #pragma unroll
                     for (int j = 0; j < 64; ++j) y[j] -= d;
@@ -1604,7 +1615,7 @@ __global__ void __launch_bounds__(Rows<FP8, D>::THREADS, 1)
                     float terms[3][16];
 #pragma unroll
                     for (int j = 0; j < 64; j += 4) {
-                        const float hold = sv[j / 16] * (float)(1 << S::HELD);
+                        const float hold = sv[j / 16] * power2(S::HELD);
                         uint32_t a[3], d[3];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
@@ -1663,7 +1674,7 @@ __global__ void __launch_bounds__(Rows<FP8, D>::THREADS, 1)
             const float ref = fmaxf(ms[0], ms[RB]);
             float f0 = ex2(ms[0] - ref), f1 = ex2(ms[RB] - ref);
             const float sum = fmaf(ls[RB], f1, ls[0] * f0);
-            const float scale = (pieces == 1 ? 1.f / sum : 1.f) * (1.f / (1 << S::HELD));
+            const float scale = (pieces == 1 ? 1.f / sum : 1.f) * power2(-S::HELD);
             f0 *= scale;
             f1 *= scale;
             float *const piece = p.work + (size_t)(2 * blockIdx.x + ((int)blockIdx.x > cf)) * S::PIECE;

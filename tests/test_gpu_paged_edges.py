@@ -1,5 +1,5 @@
 """The paged cache at the ends of its range, against the 64-bit oracle: keys
-of any size, pages that are missing for whole tiles.  Tolerances:
+and V scales of any size, pages that are missing for whole tiles.  Tolerances:
 tests/test_gpu_paged.py, and tests/paged_case.py for the attention.
 """
 import numpy as np
@@ -91,3 +91,16 @@ def test_tiles_of_missing_pages(dsa, kv_type, zero, lens, new, gone):
         codes = kv.pages.contiguous().view(torch.uint8).cpu().numpy().reshape(c.codes.shape)
         values[:n] = ref.e4m3_decode(codes) * kv.scales.double().cpu().numpy()[:, :, None, :, None]
     attended(c, kv, values, table, dsa.DSA_OK if zero else dsa.DSA_ERR_DEVICE_CHECK)
+
+
+# ---- V scales ---------------------------------------------------------------
+
+@pytest.mark.parametrize("e", [-72, 100, 119])
+@pytest.mark.parametrize("new", [1, 6, 40])
+def test_weights_beside_v_scales_of_any_size(dsa, e, new):
+    """V scales at both ends: the sum of the weights keeps the small ones."""
+    c = Case("fp8e4m3", 8, 2, 64, 16, [900, 300], [new, new], seed=4)
+    c.codes = np.where(c.codes & 0x7f > 0x70, 0x30, c.codes).astype(np.uint8)  # up to 128; every slot a value
+    c.scales[:, :, 1] = 2.0 ** e
+    c.q *= 3
+    attended(c, c.cache(), ref.e4m3_decode(c.codes) * c.scales[:, :, None, :, None])
