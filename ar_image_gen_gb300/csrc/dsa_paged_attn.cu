@@ -68,7 +68,10 @@ constexpr int kSoft = 128;     // threads of a softmax group: one per key of a t
 constexpr uint32_t kSoftBar = 1;  // named barrier of the first softmax group
 constexpr int kTile = 128;     // keys of a tile
 constexpr uint32_t kBox = kTile * 128;  // bytes of one 128-byte column of a tile
-constexpr float kNoMax = -1e30f;
+// Reference of a published row that no logit above -infinity has set, and of
+// rows that a group has beyond its block: they weigh nothing and set none.
+constexpr float kNoMax = -3.402823466e38f;
+constexpr float kNever = 1e30f;
 // Of an E4M3 cache the reference is log2 of the largest weight x V scale, less
 // this.  A row's sum adds up the weights themselves, 2^kLow over the V scale of
 // the page that set the reference: with scales of 2^-72 to 2^120 from 2^-102,
@@ -1027,6 +1030,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
             float l[RW], mr[RW];
 #pragma unroll
             for (int r = 0; r < RW; ++r) l[r] = mr[r] = 0.f;
+            uint32_t open = (1u << nr) - 1;  // rows whose reference no logit has set yet: any above -infinity will
             bool stop = false;
             for (int t = t0; t < t1; ++t, ++g) {
                 const int b = g & 1;
@@ -1083,7 +1087,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                     tops[r % 4] = fmaxf(tops[r % 4], y[r]);
                 }
                 const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                bool need = t == t0;
+                bool need = t == t0 || open;
                 if (!need) need = named_bar_or(bar, kSoft, top > (float)(S::SLACK + S::LOW) - ev || fail);
                 if (need) {
                     // New references: each row's largest logit + log2(V scale), where that has grown past the slack.
@@ -1098,6 +1102,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                     }
                     if (t > t0) fail = fail || !wait_poll(pv_done + 8 * (b ^ 1), (uint32_t)((g - 1) >> 1) & 1u, p.wait_limit);
                     tc_fence_after();
+                    uint32_t shut = 0;
 #pragma unroll
                     for (int c0 = 0; c0 < RW; c0 += 8) {
                         if (c0 >= nr) break;
@@ -1127,10 +1132,11 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                             f[i] = 1.f;
                             if (i % GR == 0 && r >= nr) break;
                             // rows beyond the block never ask for more (and weigh nothing)
-                            const float held = mr[r], old = t == t0 ? kNoMax : held;
-                            const float low = best[i] - (float)S::LOW;
-                            const float now = r >= nr ? -kNoMax : low > old + (float)S::SLACK ? low : old;
-                            if (now != old && r < nr) f[i] = ex2(old - now), any = true;
+                            const float held = mr[r], old = open >> r & 1 ? -INFINITY : held, low = best[i] - (float)S::LOW;
+                            const bool grow = low > old + (float)S::SLACK && r < nr;
+                            const float now = r >= nr ? kNever : grow ? low : held;
+                            if (grow) f[i] = ex2(old - now), any = true;
+                            shut |= (uint32_t)grow << r;
                             y[r] += held - now;
                             mr[r] = now;
                             l[r] *= f[i];
@@ -1158,6 +1164,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                             }
                         }
                     }
+                    open &= ~shut;
                 }
                 // The buffer of the weights is free once tile g - 2 is done.
                 if (g >= 2) fail = fail || !wait_poll(pv_done + 8 * b, (uint32_t)((g - 2) >> 1) & 1u, p.wait_limit);
@@ -1222,7 +1229,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
             if (tid == 0) {
 #pragma unroll
                 for (int r = 0; r < RW; ++r)
-                    if (r < nr) ms[r] = mr[r];
+                    if (r < nr) ms[r] = open >> r & 1 ? kNoMax : mr[r];
             }
         }
         if (fail) atomicOr(p.b.status, ST_TIMEOUT);
@@ -1547,6 +1554,7 @@ __global__ void __launch_bounds__(Rows<FP8, D>::THREADS, 1)
             const float c = row < nr ? qc[buf * RB + row] : 0.f;
             const int bnd = bound[buf * RB + row];
             float m = 0.f, l = 0.f;
+            bool open = row < nr;  // no logit has set the reference yet: any above -infinity will
             for (int t = t0; t < t1; ++t, ++g) {
                 const int b = g & 1;
                 const int key0 = t * kTile + half * 64;
@@ -1587,15 +1595,15 @@ __global__ void __launch_bounds__(Rows<FP8, D>::THREADS, 1)
                     }
                     top = fmaxf(top, fmaxf(a, d) + ev[j]);
                 }
-                const bool grow = t == t0 || top > (float)(S::SLACK + S::LOW);
+                const bool grow = top > (open ? -INFINITY : (float)(S::SLACK + S::LOW));
                 if (__any_sync(0xffffffffu, grow)) {
                     // A new reference where the largest logit + log2(V scale) of the row has grown past the slack.
-                    const float d = !grow ? 0.f : (t == t0 ? fmaxf(top, kNoMax) : top) - (float)S::LOW;
+                    const float d = grow ? top - (float)S::LOW : 0.f;
                     m += d;
 #pragma unroll
                     for (int j = 0; j < 64; ++j) y[j] -= d;
                     if (t > t0) {
-                        const float f = ex2(-d);
+                        const float f = open && grow ? 0.f : ex2(-d);
                         l *= f;
                         fail = fail || !wait_poll(pv_done + 16 * half + 8 * (b ^ 1), (uint32_t)((g - 1) >> 1) & 1u, p.wait_limit);
                         __syncwarp();
@@ -1609,6 +1617,7 @@ __global__ void __launch_bounds__(Rows<FP8, D>::THREADS, 1)
                             tmem_st16(at + i, o);
                         }
                     }
+                    if (grow) open = false;
                 }
                 // Weights, over the logits they come from.
                 if (FP8) {
@@ -1664,7 +1673,7 @@ __global__ void __launch_bounds__(Rows<FP8, D>::THREADS, 1)
             }
 
             // ---- the item's rows, or its piece of them; half of the columns each
-            refs[((k & 1) * 2 + half) * RB + row] = m;
+            refs[((k & 1) * 2 + half) * RB + row] = open ? kNoMax : m;
             sums[((k & 1) * 2 + half) * RB + row] = l;
             for (int i = 0; i < 2; ++i)
                 fail = fail || !wait_poll(pv_done + 16 * i + 8 * ((g - 1) & 1), (uint32_t)((g - 1) >> 1) & 1u, p.wait_limit);

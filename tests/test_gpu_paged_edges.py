@@ -1,6 +1,7 @@
 """The paged cache at the ends of its range, against the 64-bit oracle: keys
-and V scales of any size, pages that are missing for whole tiles.  Tolerances:
-tests/test_gpu_paged.py, and tests/paged_case.py for the attention.
+and V scales of any size, pages that are missing for whole tiles, tiles whose
+logits leave nothing.  Tolerances: tests/test_gpu_paged.py, and
+tests/paged_case.py for the attention.
 """
 import numpy as np
 import pytest
@@ -104,3 +105,44 @@ def test_weights_beside_v_scales_of_any_size(dsa, e, new):
     c.scales[:, :, 1] = 2.0 ** e
     c.q *= 3
     attended(c, c.cache(), ref.e4m3_decode(c.codes) * c.scales[:, :, None, :, None])
+
+
+# ---- logits that leave nothing ----------------------------------------------
+
+@pytest.mark.parametrize("Hq,Hk,new", [(3, 3, 1), (8, 2, 1), (12, 1, 1), (8, 2, 40)])
+@pytest.mark.parametrize("n,hidden", [(600, 128), (600, 300), (20000, 9000), (700, 0)])
+def test_tiles_whose_logits_are_minus_infinity(dsa, Hq, Hk, new, n, hidden):
+    """Keys of minus infinity weigh nothing, also where they fill the first tiles of a row or all of a piece."""
+    c = Case("bf16", Hq, Hk, 64, 16, [n], [new], seed=6)
+    kv = c.cache()
+    cu, lens, table = c.batch()
+    kv.append(None, c.k.cuda(), c.v.cuda(), cu, lens, table)
+    c.q[:, :, 0] = 1
+    values = kv.pages.double().cpu().numpy()
+    for t in range(hidden):
+        kv.pages[c.table[0, t // 16], :, t % 16, 0, 0] = float("-inf")
+    values = kv.pages.double().cpu().numpy()
+    attended(c, kv, values)
+
+
+@pytest.mark.parametrize("kv_type", ["bf16", "fp8e4m3"])
+@pytest.mark.parametrize("Hq,Hk,new", [(3, 3, 1), (8, 2, 1), (8, 2, 40)])
+def test_logits_far_below_zero(dsa, kv_type, Hq, Hk, new):
+    """Finite logits of -1e33 and less: the largest takes the row."""
+    n = 300
+    c = Case(kv_type, Hq, Hk, 64, 16, [n], [new], seed=6)
+    c.q[:] = 0
+    c.q[:, :, 0] = 2
+    kv = c.cache()
+    cu, lens, table = c.batch()
+    k = torch.zeros((n, Hk, 64))
+    k[:, :, 0] = -(1e34 * 2.0 ** torch.linspace(0, 8, n))[:, None]
+    v = torch.randn((n, Hk, 64), generator=torch.Generator().manual_seed(0))
+    kv.append(None, k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16).cuda(), torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+              lens, table)
+    if kv_type == "bf16":
+        values = kv.pages.double().cpu().numpy()
+    else:
+        codes = kv.pages.contiguous().view(torch.uint8).cpu().numpy().reshape(c.codes.shape)
+        values = ref.e4m3_decode(codes) * kv.scales.double().cpu().numpy()[:, :, None, :, None]
+    attended(c, kv, values)
