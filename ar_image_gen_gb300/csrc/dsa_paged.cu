@@ -437,6 +437,19 @@ int make_batch(dsa_paged_ctx *h, int n_seqs, int n_tokens, const int32_t *cu, co
     return DSA_OK;
 }
 
+// Memory of the device that the handle is made on: a kernel launched there
+// would follow a pointer of another device, or of the host, all the same.
+int check_memory(const char *name, const void *p, int device)
+{
+    cudaPointerAttributes a;
+    cudaError_t e = cudaPointerGetAttributes(&a, p);
+    if (e != cudaSuccess) return cuda_fail(e, "pointer query");
+    if (a.type == cudaMemoryTypeManaged || (a.type == cudaMemoryTypeDevice && a.device == device)) return DSA_OK;
+    if (a.type == cudaMemoryTypeDevice)
+        return fail(DSA_ERR_ARG, "%s lie on device %d, the current one is %d", name, a.device, device);
+    return fail(DSA_ERR_ARG, "%s must be device memory", name);
+}
+
 int check_stride(const char *name, int64_t stride, int64_t row)
 {
     if (stride < row || stride % 8 || stride > LLONG_MAX / 16 / INT_MAX)
@@ -488,7 +501,9 @@ int dsa_paged_create(int q_heads, int kv_heads, int head_dim, int page_size, int
         free_paged(h);
         return cuda_fail(e, "device query");
     }
-    int rc = dev_alloc((void **)&h->status, 16, "paged cache status");
+    int rc = check_memory("pages", pages, h->device);
+    if (rc == DSA_OK && scales) rc = check_memory("scales", scales, h->device);
+    if (rc == DSA_OK) rc = dev_alloc((void **)&h->status, 16, "paged cache status");
     if (rc == DSA_OK && (e = cudaMemset(h->status, 0, 16)) != cudaSuccess) rc = cuda_fail(e, "cudaMemset");
     if (rc == DSA_OK) rc = dsa_detail::paged_attn_init(h);
     if (rc != DSA_OK) {

@@ -533,6 +533,10 @@ class PagedKV:
         if eight and (tuple(scales.shape) != (num_pages, kv_heads, 2) or scales.dtype != torch.float32
                       or not scales.is_cuda or not scales.is_contiguous()):
             raise ValueError(f"scales must be a contiguous CUDA float32 tensor {(num_pages, kv_heads, 2)}")
+        # the handle, its workspace and its kernels are the current device's
+        _on_current_device(pages.get_device())
+        if eight and scales.get_device() != pages.get_device():
+            raise ValueError(f"pages are on CUDA device {pages.get_device()}, scales on {scales.get_device()}")
         code, h = dsa_paged_create(q_heads, kv_heads, head_dim, page_size, num_pages, DTYPES[dtype], pages, scales)
         _check(code, "dsa_paged_create")
         self.h, self.pages, self.scales, self.device = h, pages, scales, pages.get_device()

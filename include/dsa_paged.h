@@ -58,7 +58,7 @@ typedef struct dsa_paged_ctx *dsa_paged; /* opaque; library-owned */
  * h / (q_heads / kv_heads)), kv_heads in [1, 1024]; head_dim 64 or 128;
  * page_size 16, 32, 64 or 128; num_pages >= 1 with num_pages * kv_heads *
  * page_size < 2^31; dtype DSA_BF16 or DSA_FP8_E4M3; pages 128-byte aligned,
- * scales 16-byte aligned (NULL for DSA_BF16).  The pool must outlive the
+ * scales 16-byte aligned (NULL for DSA_BF16), both on the current device.  The pool must outlive the
  * handle; its contents are the caller's to copy, share between sequences
  * (pages of a common prefix) or give to another sequence.  Allocates on the
  * current device a workspace for pieces of long sequences (at most 24 MiB)

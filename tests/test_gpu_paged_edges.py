@@ -1,6 +1,6 @@
 """The paged cache at the ends of its range, against the 64-bit oracle: keys
 and V scales of any size, pages that are missing for whole tiles, tiles whose
-logits leave nothing.  Tolerances: tests/test_gpu_paged.py, and
+logits leave nothing, pools that are no device memory.  Tolerances: tests/test_gpu_paged.py, and
 tests/paged_case.py for the attention.
 """
 import numpy as np
@@ -146,3 +146,18 @@ def test_logits_far_below_zero(dsa, kv_type, Hq, Hk, new):
         codes = kv.pages.contiguous().view(torch.uint8).cpu().numpy().reshape(c.codes.shape)
         values = ref.e4m3_decode(codes) * kv.scales.double().cpu().numpy()[:, :, None, :, None]
     attended(c, kv, values)
+
+
+# ---- whose memory a pool is --------------------------------------------------
+
+def test_a_pool_is_memory_of_the_current_device(dsa):
+    """Host memory is refused where it can be told; memory of another device likewise (two devices at least)."""
+    host = np.zeros(1 << 16, dtype=np.uint8)
+    at = (host.ctypes.data + 127) // 128 * 128
+    scales = torch.ones((1, 1, 2), device="cuda")
+    pages = torch.zeros(1 << 13, dtype=torch.uint8, device="cuda")
+    for p, s in ((at, scales), (pages, at)):
+        code, h = dsa.dsa_paged_create(1, 1, 64, 16, 1, dsa.DSA_FP8_E4M3, p, s)
+        assert code == dsa.DSA_ERR_ARG and not h.value and dsa.dsa_last_error()
+    code, h = dsa.dsa_paged_create(1, 1, 64, 16, 1, dsa.DSA_FP8_E4M3, pages, scales)
+    assert code == dsa.DSA_OK and dsa.dsa_paged_destroy(h) == dsa.DSA_OK

@@ -1,9 +1,51 @@
-"""The oracle of the paged cache at the ends of its range, on the CPU."""
+"""The paged cache on the CPU: what its Python form refuses before it reaches
+the library, with a fake pool of another device, and the oracle at the ends of
+its range."""
 from fractions import Fraction
 
 import numpy as np
+import pytest
+import torch
 
 from oracle import paged as ref
+
+
+@pytest.fixture(scope="module")
+def dsa():
+    from __graft_entry__ import build
+    build()
+    from ar_image_gen_gb300 import dsa as mod
+    return mod
+
+
+class FakePool:
+    """Shape, type and place of a CUDA tensor."""
+
+    def __init__(self, shape, dtype, device):
+        self.shape, self.dtype, self.device_index, self.is_cuda = torch.Size(shape), dtype, device, True
+
+    def get_device(self):
+        return self.device_index
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+@pytest.mark.parametrize("pages,scales", [(1, 1), (1, 0), (0, 1)])
+def test_a_pool_of_another_device_is_refused(dsa, monkeypatch, pages, scales):
+    """Before anything is made on the current device, 0."""
+    monkeypatch.setattr(dsa, "_current_device", lambda: 0)
+
+    def never(*a):
+        raise AssertionError("reached the library")
+
+    monkeypatch.setattr(dsa, "dsa_paged_create", never)
+    with pytest.raises(ValueError):
+        dsa.PagedKV(2, 2, 64, 16, 3, "fp8e4m3", pages=FakePool((3, 2, 16, 2, 64), torch.float8_e4m3fn, pages),
+                    scales=FakePool((3, 2, 2), torch.float32, scales))
 
 
 def test_the_oracle_takes_keys_of_any_size():
