@@ -622,10 +622,7 @@ int dsa_paged_sync_status(dsa_paged h, void *stream)
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
     if (e != cudaSuccess) return cuda_fail(e, "status copy");
     if (word == 0) return DSA_OK;
-    // A launch that gave up may leave counters of shared pieces part-way.
-    if ((e = cudaMemsetAsync(h->status, 0, 16, st)) != cudaSuccess ||
-        (h->counters && (e = cudaMemsetAsync(h->counters, 0, sizeof(int) * dsa_paged_k::kCounters, st)) != cudaSuccess) ||
-        (e = cudaStreamSynchronize(st)) != cudaSuccess)
+    if ((e = cudaMemsetAsync(h->status, 0, 16, st)) != cudaSuccess || (e = cudaStreamSynchronize(st)) != cudaSuccess)
         return cuda_fail(e, "status reset");
     if (word & dsa_paged_k::ST_TIMEOUT) return fail(DSA_ERR_TIMEOUT, "a bounded wait in the paged attention gave up");
     return fail(DSA_ERR_DEVICE_CHECK, "a sequence of the batch does not fit it, or a page number lies outside the pool");

@@ -109,6 +109,15 @@ struct Info {
     int first, pieces;   // CTA of the item's first tile; CTAs that share the item
 };
 
+// Words of a CTA beside its items'.
+struct Shared {
+    uint32_t tmem;   // address of its tensor memory
+    int last[2];     // of each group: its piece of the shared item came last
+    int arrived[2];  // shared items whose counters the groups have added to
+    int gave_up;     // a group has left items undone
+    int pad[2];
+};
+
 template <bool FP8, int D, int RB>
 struct Shape {
     static constexpr int EB = FP8 ? 1 : 2;
@@ -155,7 +164,7 @@ struct Shape {
     // of 64, 37.5 us and 39.4; 4 x 20000 keys 32.5 and 35.3.
     static constexpr int CTAS = RB <= 8 || (RB == 16 && FP8) ? 2 : 1;
     static constexpr uint32_t ROWF = (3 * QD + 8 + 8 + 2) * (RB < 8 ? 8 : RB);  // qc, bound, orow [QD], wmax, lsum [2][4], m [2]
-    static constexpr uint32_t FIXED = QD * QBUF + 2 * PBUF + kBarBytes + kScaleRing * 64 + ROWF * 4 + QD * sizeof(Info) + 16 + 1024;
+    static constexpr uint32_t FIXED = QD * QBUF + 2 * PBUF + kBarBytes + kScaleRing * 64 + ROWF * 4 + QD * sizeof(Info) + sizeof(Shared) + 1024;
     static constexpr uint32_t ROOM = (228 * 1024) / CTAS - 1024 - 256;
     static constexpr int SLOTS = (ROOM - FIXED) / SLOT > 8 ? 8 : (ROOM - FIXED) / SLOT;
     static constexpr uint32_t OFF_Q = SLOTS * SLOT;
@@ -164,7 +173,7 @@ struct Shape {
     static constexpr uint32_t OFF_SC = OFF_BAR + kBarBytes;      // [kScaleRing][8][2] page scales
     static constexpr uint32_t OFF_ROW = OFF_SC + kScaleRing * 64;
     static constexpr uint32_t OFF_INFO = OFF_ROW + ROWF * 4;
-    static constexpr uint32_t SMEM = OFF_INFO + QD * sizeof(Info) + 16 + 1024;  // TMEM address, flags; alignment slack
+    static constexpr uint32_t SMEM = OFF_INFO + QD * sizeof(Info) + sizeof(Shared) + 1024;  // TMEM address, flags; alignment slack
     static_assert(SLOTS >= PARTS + 1 && (2 * SLOTS + 7 * GROUPS + 2 * QD) * 8 <= (int)kBarBytes, "slots of K and V");
     static_assert(SMEM <= ROOM && TCOLS <= TMEM && TMEM * CTAS <= 512, "shared and tensor memory of a CTA");
 };
@@ -235,6 +244,7 @@ struct Item {
     int rb, head;
     int tiles, t0, t1, weight;
     long long x;         // place of its first tile
+    __device__ __forceinline__ bool split() const { return t0 > 0 || t1 < tiles; }  // other CTAs have tiles of it
 };
 
 // Walks the items of a run [x0, x1) of the cost line: an item takes item_lead,
@@ -561,12 +571,21 @@ __device__ __forceinline__ void put_info(Info &f, const Item &cur, int nr, bool 
         f.least = cur.len - cur.n + p.over_g(cur.rb * RB) + 1;
         f.first = blockIdx.x;
         f.pieces = 1;
-        if (cur.t0 > 0 || cur.t1 < cur.tiles) {
+        if (cur.split()) {
             // The CTA whose run [total c / workers, ..) holds place x: the last with total c / workers <= x.
             f.first = (int)(((cur.x + 1) * workers + total - 1) / total) - 1;
             f.pieces = (int)(((cur.x + (long long)(cur.tiles - 1) * cur.weight + 1) * workers + total - 1) / total) - f.first;
         }
     }
+}
+
+// Adds a piece of a shared item to its counter; the last of them leaves it at
+// 0 for the next launch.
+__device__ __forceinline__ bool arrive(int *counter, int pieces)
+{
+    const bool last = atomicAdd(counter, 1) == pieces - 1;
+    if (last) *counter = 0;
+    return last;
 }
 
 // Joins the pieces of row r of an item whose first piece is of CTA cf, in the
@@ -714,6 +733,29 @@ __device__ void find_run(const AttnParams &p, long long &x0, long long &x1, int 
     }
 }
 
+// A CTA whose waits gave up adds its pieces all the same: a counter left
+// part-way would make a later launch join pieces that are not there yet.  All
+// threads call it, after the CTA's last barrier; it finds the run anew, which
+// then need not be kept in registers for it.
+template <int RB, int kThreads, int groups>
+__device__ __noinline__ void arrive_late(const AttnParams &p, const int *arrived)
+{
+    long long x0, x1, base = 0, total;
+    int seq = 0, workers;
+    find_run<RB, kThreads>(p, x0, x1, seq, base, total, workers);
+    if (threadIdx.x != 0) return;
+    Walk<RB> walk(p, x0, x1, seq, base);
+    Item it;
+    Info f;
+    for (int j = 0; walk.next(it);) {
+        if (!it.split()) continue;
+        put_info<RB>(f, it, 0, true, false, p, workers, total);
+        for (int i = 0; i < groups; ++i)
+            if (j >= arrived[i]) arrive(p.counters + f.first * groups + i, f.pieces);
+        ++j;
+    }
+}
+
 template <bool FP8, int D, int RB>
 __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>::CTAS)
     attn_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttnParams p)
@@ -741,8 +783,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
     float *const lsum = wmax + 8 * GS;                               // [2][4][GS] sums of weights, by item parity
     float *const mref = lsum + 8 * GS;                               // [2][GS] references, by item parity
     Info *const info = reinterpret_cast<Info *>(smem + S::OFF_INFO);
-    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(info + S::QD);
-    int *const last_flag = reinterpret_cast<int *>(tmem_slot + 1);
+    Shared &sh = *reinterpret_cast<Shared *>(info + S::QD);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < SLOTS; ++s) {
@@ -762,17 +803,18 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
             mbar_init(q_ready + 8 * i, 1);
             mbar_init(i_free + 8 * i, 4 * S::GROUPS);
         }
+        sh.arrived[0] = sh.arrived[1] = sh.gave_up = 0;
         fence_barrier_init();
         prefetch_tmap(&map);
     }
     if (warp == 2) {
-        tmem_alloc(smem_u32(tmem_slot), S::TMEM);
+        tmem_alloc(smem_u32(&sh.tmem), S::TMEM);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = sh.tmem;
 
     pdl_wait();
     pdl_launch_dependents();
@@ -995,13 +1037,11 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                 __threadfence();
                 named_bar_sync(bar, kSoft);
                 if (tid == 0) {
-                    int *const counter = p.counters + cf * S::GROUPS + group;
-                    const int done = atomicAdd(counter, 1);
-                    last_flag[group] = done == pieces - 1;
-                    if (done == pieces - 1) *counter = 0;  // for the next launch
+                    sh.last[group] = arrive(p.counters + cf * S::GROUPS + group, pieces);
+                    ++sh.arrived[group];
                 }
                 named_bar_sync(bar, kSoft);
-                if (last_flag[group]) {
+                if (sh.last[group]) {
                     // Joins the pieces in the order of their keys.
                     __threadfence();
                     for (int r = wg; r < nr; r += 4)
@@ -1232,7 +1272,10 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
                     if (r < nr) ms[r] = open >> r & 1 ? kNoMax : mr[r];
             }
         }
-        if (fail) atomicOr(p.b.status, ST_TIMEOUT);
+        if (fail) {
+            atomicOr(p.b.status, ST_TIMEOUT);
+            sh.gave_up = 1;
+        }
     }
 
     __syncthreads();
@@ -1246,6 +1289,7 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
         tc_fence_after();
         tmem_dealloc(tmem, S::TMEM);
     }
+    if (sh.gave_up) arrive_late<RB, S::THREADS, S::GROUPS>(p, sh.arrived);
 }
 
 // ---------------------------------------------------------------------------
@@ -1307,7 +1351,7 @@ struct Rows {
     static constexpr int SLACK = FP8 ? 6 : 8, LOW = FP8 ? kLow : 0, HELD = FP8 ? 15 - SLACK - LOW : 0;  // fp16 reaches 2^16
     static constexpr int PIECE = RB * (D + 2);
     static constexpr uint32_t ROWF = (3 * QD + 4 + 4) * RB;  // qc, bound, orow [QD], refs [2][2], sums [2][2]
-    static constexpr uint32_t FIXED = QD * QBUF + kBarBytes + kScaleRing * 64 + ROWF * 4 + QD * sizeof(Info) + 16 + 1024;
+    static constexpr uint32_t FIXED = QD * QBUF + kBarBytes + kScaleRing * 64 + ROWF * 4 + QD * sizeof(Info) + sizeof(Shared) + 1024;
     static constexpr uint32_t ROOM = 228 * 1024 - 1024 - 256;
     static constexpr int SLOTS = (ROOM - FIXED) / SLOT > 8 ? 8 : (ROOM - FIXED) / SLOT;
     static constexpr uint32_t OFF_Q = SLOTS * SLOT;
@@ -1315,7 +1359,7 @@ struct Rows {
     static constexpr uint32_t OFF_SC = OFF_BAR + kBarBytes;
     static constexpr uint32_t OFF_ROW = OFF_SC + kScaleRing * 64;
     static constexpr uint32_t OFF_INFO = OFF_ROW + ROWF * 4;
-    static constexpr uint32_t SMEM = OFF_INFO + QD * sizeof(Info) + 16 + 1024;
+    static constexpr uint32_t SMEM = OFF_INFO + QD * sizeof(Info) + sizeof(Shared) + 1024;
     static_assert(SLOTS >= PARTS + 1 && (2 * SLOTS + 11 + 2 * QD) * 8 <= (int)kBarBytes, "slots of K and V");
     static_assert(SMEM <= ROOM, "shared memory of a CTA");
 };
@@ -1340,8 +1384,7 @@ __global__ void __launch_bounds__(Rows<FP8, D>::THREADS, 1)
     float *const refs = qc + 3 * S::QD * RB;                                   // [2][2][RB] by item parity and half
     float *const sums = refs + 4 * RB;                                         // [2][2][RB] by item parity and half
     Info *const info = reinterpret_cast<Info *>(smem + S::OFF_INFO);
-    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(info + S::QD);
-    int *const last_flag = reinterpret_cast<int *>(tmem_slot + 1);
+    Shared &sh = *reinterpret_cast<Shared *>(info + S::QD);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -1361,17 +1404,18 @@ __global__ void __launch_bounds__(Rows<FP8, D>::THREADS, 1)
             mbar_init(q_ready + 8 * i, 2);  // one arrival a query warp
             mbar_init(i_free + 8 * i, 8);
         }
+        sh.arrived[0] = sh.arrived[1] = sh.gave_up = 0;
         fence_barrier_init();
         prefetch_tmap(&map);
     }
     if (warp == 3) {
-        tmem_alloc(smem_u32(tmem_slot), S::TMEM);
+        tmem_alloc(smem_u32(&sh.tmem), S::TMEM);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = sh.tmem;
     const uint32_t o_col = tmem + 256;
 
     pdl_wait();
@@ -1725,12 +1769,11 @@ __global__ void __launch_bounds__(Rows<FP8, D>::THREADS, 1)
                 __threadfence();
                 named_bar_sync(kSoftBar, 256);
                 if (sw == 0 && lane == 0) {
-                    const int done = atomicAdd(p.counters + cf, 1);
-                    *last_flag = done == pieces - 1;
-                    if (done == pieces - 1) p.counters[cf] = 0;  // for the next launch
+                    sh.last[0] = arrive(p.counters + cf, pieces);
+                    ++sh.arrived[0];
                 }
                 named_bar_sync(kSoftBar, 256);
-                if (*last_flag) {
+                if (sh.last[0]) {
                     __threadfence();
                     for (int r = sw; r < nr; r += 8)
                         join_row<D, RB, 4>(p.work, S::PIECE, cf, pieces, r, p.out + (size_t)to[r] * D);
@@ -1739,7 +1782,10 @@ __global__ void __launch_bounds__(Rows<FP8, D>::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(i_free + 8 * buf);
         }
-        if (fail) atomicOr(p.b.status, ST_TIMEOUT);
+        if (fail) {
+            atomicOr(p.b.status, ST_TIMEOUT);
+            sh.gave_up = 1;
+        }
     }
 
     __syncthreads();
@@ -1753,6 +1799,7 @@ __global__ void __launch_bounds__(Rows<FP8, D>::THREADS, 1)
         tc_fence_after();
         tmem_dealloc(tmem, S::TMEM);
     }
+    if (sh.gave_up) arrive_late<RB, S::THREADS, 1>(p, sh.arrived);
 }
 
 }  // namespace dsa_paged_k

@@ -1,6 +1,7 @@
 """The paged cache at the ends of its range, against the 64-bit oracle: keys
 and V scales of any size, pages that are missing for whole tiles, tiles whose
-logits leave nothing, pools that are no device memory.  Tolerances: tests/test_gpu_paged.py, and
+logits leave nothing, calls after one that gave up and beside a reading of the status,
+pools that are no device memory.  Tolerances: tests/test_gpu_paged.py, and
 tests/paged_case.py for the attention.
 """
 import numpy as np
@@ -146,6 +147,60 @@ def test_logits_far_below_zero(dsa, kv_type, Hq, Hk, new):
         codes = kv.pages.contiguous().view(torch.uint8).cpu().numpy().reshape(c.codes.shape)
         values = ref.e4m3_decode(codes) * kv.scales.double().cpu().numpy()[:, :, None, :, None]
     attended(c, kv, values)
+
+
+# ---- after a call that gave up ----------------------------------------------
+
+@pytest.mark.parametrize("kv_type,Hq,new,n_seqs", [("bf16", 1, 1, 800), ("fp8e4m3", 1, 1, 800), ("fp8e4m3", 4, 8, 400),
+                                                   ("bf16", 8, 16, 300), ("fp8e4m3", 8, 16, 300)])
+def test_a_call_after_one_that_gave_up(dsa, kv_type, Hq, new, n_seqs):
+    """Several items a CTA, some of whose waits give up: the next call is whole, whether or not the status was read."""
+    c = Case(kv_type, Hq, 1, 128, 16, [1500], [new], seed=2)
+    kv = c.cache()
+    _, lens, table = c.batch()
+    kv.append(None, c.k.cuda(), c.v.cuda(), *c.batch())
+    batch = torch.arange(n_seqs + 1, dtype=torch.int32, device="cuda") * new, lens.repeat(n_seqs), table.repeat(n_seqs, 1)
+    q = c.q.cuda().repeat(n_seqs, 1, 1)
+    first, out = torch.empty_like(q), torch.empty_like(q)
+    kv.attend(q, *batch, first, max_new=new)
+    assert kv.sync_status() == dsa.DSA_OK
+    for limit in (0, 1, 2, 3, 4, 6) * 3:
+        kv.attend(-q, *batch, out, max_new=new)  # what the workspace holds is of other queries
+        kv.set_wait_limit(limit)
+        kv.attend(-q, *batch, out, max_new=new)
+        kv.set_wait_limit(0xffffffff)
+        kv.attend(q, *batch, out, max_new=new)
+        assert torch.equal(out, first), limit
+    assert kv.sync_status() == dsa.DSA_ERR_TIMEOUT
+    assert kv.sync_status() == dsa.DSA_OK
+
+
+def test_reading_the_status_leaves_a_running_call_alone(dsa):
+    """A bad append on one stream, an attention on another: what the first did is read while the second runs."""
+    n_seqs = 800
+    c = Case("bf16", 1, 1, 128, 16, [6000], [1], seed=2)
+    kv = c.cache()
+    _, lens, table = c.batch()
+    k, v = c.k.cuda(), c.v.cuda()
+    kv.append(None, k, v, *c.batch())
+    batch = torch.arange(n_seqs + 1, dtype=torch.int32, device="cuda"), lens.repeat(n_seqs), table.repeat(n_seqs, 1)
+    q = c.q.cuda().repeat(n_seqs, 1, 1)
+    first, out = torch.empty_like(q), torch.empty_like(q)
+    kv.attend(q, *batch, first, max_new=1)
+    assert kv.sync_status() == dsa.DSA_OK
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    bad = torch.tensor([0, 1], dtype=torch.int32, device="cuda"), torch.tensor([-1], dtype=torch.int32, device="cuda"), table
+    torch.cuda.synchronize()
+    for _ in range(20):
+        out.fill_(7.0)
+        torch.cuda.synchronize()
+        kv.append(None, k, v, *bad, stream=a)
+        a.synchronize()
+        kv.attend(q, *batch, out, max_new=1, stream=b)
+        assert kv.sync_status(a) == dsa.DSA_ERR_DEVICE_CHECK
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+    assert kv.sync_status() == dsa.DSA_OK
 
 
 # ---- whose memory a pool is --------------------------------------------------
