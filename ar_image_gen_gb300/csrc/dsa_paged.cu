@@ -385,6 +385,10 @@ __global__ void __launch_bounds__(kAppendThreads, FP8 ? 3 : 4) append_kernel(con
     }
 }
 
+// Resets the error that the host has read and no other: one of the other kind,
+// or of a call on another stream, is still to be read.
+__global__ void clear_status(int *status, int bit) { atomicAnd(status, ~bit); }
+
 }  // namespace dsa_paged_k
 
 using dsa_detail::cuda_fail;
@@ -622,9 +626,11 @@ int dsa_paged_sync_status(dsa_paged h, void *stream)
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
     if (e != cudaSuccess) return cuda_fail(e, "status copy");
     if (word == 0) return DSA_OK;
-    if ((e = cudaMemsetAsync(h->status, 0, 16, st)) != cudaSuccess || (e = cudaStreamSynchronize(st)) != cudaSuccess)
+    const int bit = word & dsa_paged_k::ST_TIMEOUT ? dsa_paged_k::ST_TIMEOUT : dsa_paged_k::ST_CHECK;
+    dsa_paged_k::clear_status<<<1, 1, 0, st>>>(h->status, bit);
+    if ((e = cudaGetLastError()) != cudaSuccess || (e = cudaStreamSynchronize(st)) != cudaSuccess)
         return cuda_fail(e, "status reset");
-    if (word & dsa_paged_k::ST_TIMEOUT) return fail(DSA_ERR_TIMEOUT, "a bounded wait in the paged attention gave up");
+    if (bit == dsa_paged_k::ST_TIMEOUT) return fail(DSA_ERR_TIMEOUT, "a bounded wait in the paged attention gave up");
     return fail(DSA_ERR_DEVICE_CHECK, "a sequence of the batch does not fit it, or a page number lies outside the pool");
 }
 

@@ -145,7 +145,8 @@ int dsa_paged_attend(dsa_paged h, int n_seqs, int n_tokens, int max_new, const i
  * Waits for `stream` and reports the handle's sticky device status:
  * DSA_ERR_TIMEOUT (a bounded wait of the attention gave up; the outputs of
  * that call are undefined) or DSA_ERR_DEVICE_CHECK (a sequence or page that
- * does not fit, see above).  Reading an error resets it.
+ * does not fit, see above).  Reading an error resets it; of two the timeout is
+ * reported first and the other by the next reading.
  */
 int dsa_paged_sync_status(dsa_paged h, void *stream);
 

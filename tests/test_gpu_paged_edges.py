@@ -203,6 +203,18 @@ def test_reading_the_status_leaves_a_running_call_alone(dsa):
     assert kv.sync_status() == dsa.DSA_OK
 
 
+def test_two_errors_are_read_one_after_the_other(dsa):
+    c = Case("fp8e4m3", 2, 2, 64, 16, [20, 300], [1, 1], seed=2)
+    kv = c.cache()
+    cu, lens, table = c.batch()
+    q = c.q.cuda()
+    lens[0] = -1
+    kv.set_wait_limit(0)
+    kv.attend(q, cu, lens, table, torch.empty_like(q))
+    kv.set_wait_limit(0xffffffff)
+    assert [kv.sync_status() for _ in range(3)] == [dsa.DSA_ERR_TIMEOUT, dsa.DSA_ERR_DEVICE_CHECK, dsa.DSA_OK]
+
+
 # ---- whose memory a pool is --------------------------------------------------
 
 def test_a_pool_is_memory_of_the_current_device(dsa):
