@@ -581,13 +581,17 @@ class PagedKV:
                                    _packed("table", table, (n_seqs, width), i32, dev), width, r, pp, qp, qs,
                                    k.data_ptr(), ks, v.data_ptr(), vs, op, _stream_of(dev, stream)), "dsa_paged_append")
 
-    def attend(self, q, cu, lens, table, out, max_new=1, stream=None):
+    def attend(self, q, cu, lens, table, out, max_new=None, stream=None):
         """out = causal attention of q [tokens, q_heads, head_dim] bf16 (the
         new tokens, already appended) over their sequences; `max_new`: the
-        most new tokens of a sequence (a hint for the launch)."""
+        most new tokens of a sequence (a hint for the launch; without it the
+        mean, the rows of q per sequence: of a prompt all, of a decode step
+        one)."""
         bf, i32, dev = self._bf16, self._int32, self.device
         n = q.shape[0]
         n_seqs, width = table.shape
+        if max_new is None:
+            max_new = max(1, -(-n // max(1, n_seqs)))
         shape = (n, self.q_heads, self.head_dim)
         _check(_L.dsa_paged_attend(self.h, n_seqs, n, max_new, _packed("cu", cu, (n_seqs + 1,), i32, dev),
                                    _packed("lens", lens, (n_seqs,), i32, dev),

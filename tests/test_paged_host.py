@@ -1,6 +1,7 @@
-"""The paged cache on the CPU: what its Python form refuses before it reaches
-the library, with a fake pool of another device, and the oracle at the ends of
-its range."""
+"""The paged cache on the CPU: what its Python form refuses and decides before
+it reaches the library, with CPU tensors and a fake pool of another device, and
+the oracle at the ends of its range."""
+import ctypes
 from fractions import Fraction
 
 import numpy as np
@@ -46,6 +47,42 @@ def test_a_pool_of_another_device_is_refused(dsa, monkeypatch, pages, scales):
     with pytest.raises(ValueError):
         dsa.PagedKV(2, 2, 64, 16, 3, "fp8e4m3", pages=FakePool((3, 2, 16, 2, 64), torch.float8_e4m3fn, pages),
                     scales=FakePool((3, 2, 2), torch.float32, scales))
+
+
+@pytest.fixture
+def cache(dsa, monkeypatch):
+    """A cache object over CPU tensors whose library calls are recorded, not made."""
+    calls = []
+
+    class Library:
+        def dsa_paged_attend(self, *a):
+            calls.append(a)
+            return dsa.DSA_OK
+
+        dsa_paged_append = dsa_paged_attend
+
+    monkeypatch.setattr(dsa, "_L", Library())
+    kv = dsa.PagedKV.__new__(dsa.PagedKV)
+    kv.h, kv.device, kv._bf16, kv._int32 = ctypes.c_void_p(), -1, torch.bfloat16, torch.int32
+    kv.q_heads, kv.kv_heads, kv.head_dim, kv.page_size = 4, 2, 64, 16
+    yield kv, calls
+    kv.h = None
+
+
+def batch(n_seqs, n):
+    return (torch.zeros(n_seqs + 1, dtype=torch.int32), torch.zeros(n_seqs, dtype=torch.int32),
+            torch.zeros((n_seqs, 3), dtype=torch.int32)), torch.zeros((n, 4, 64), dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("n_seqs,n,hint", [(96, 96, 1), (3, 3, 1), (4, 2, 1), (1, 500, 500), (2, 1025, 513), (32, 160, 5), (0, 0, 1),
+                                           (3, 0, 1), (0, 5, 5)])
+def test_attend_without_a_hint_takes_the_mean(dsa, cache, n_seqs, n, hint):
+    kv, calls = cache
+    (cu, lens, table), q = batch(n_seqs, n)
+    kv.attend(q, cu, lens, table, torch.zeros_like(q), stream=0)
+    assert calls[-1][3] == hint
+    kv.attend(q, cu, lens, table, torch.zeros_like(q), max_new=7, stream=0)
+    assert calls[-1][3] == 7
 
 
 def test_the_oracle_takes_keys_of_any_size():
