@@ -558,6 +558,10 @@ class PagedKV:
         """Writes rows k, v [tokens, kv_heads, head_dim] bf16 of the new
         tokens into their pages, rotated (k) by `rope` at pos [tokens, axes];
         q [tokens, q_heads, head_dim] (or None), rotated, goes to q_out."""
+        if (rope is None) != (pos is None):
+            raise ValueError("rope and pos go together")
+        if (q is None) != (q_out is None):
+            raise ValueError("q and q_out go together")
         bf, i32, dev, Hk, d = self._bf16, self._int32, self.device, self.kv_heads, self.head_dim
         n = k.shape[0]
         n_seqs, width = table.shape
@@ -565,14 +569,10 @@ class PagedKV:
         vs = _rows("v", v, n, Hk, d, bf, dev)
         qs, qp, op = 0, None, None
         if q is not None:
-            if q_out is None:
-                raise ValueError("q needs q_out")
             qs, qp = _rows("q", q, n, self.q_heads, d, bf, dev), q.data_ptr()
             op = _packed("q_out", q_out, (n, self.q_heads, d), bf, dev)
         r, pp = None, None
         if rope is not None:
-            if pos is None:
-                raise ValueError("rope needs pos")
             r, pp = rope.r, _packed("pos", pos, (n, rope.axes), i32, dev)
             if not r:
                 raise ValueError("the rotation plan is closed")

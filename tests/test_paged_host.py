@@ -85,6 +85,20 @@ def test_attend_without_a_hint_takes_the_mean(dsa, cache, n_seqs, n, hint):
     assert calls[-1][3] == 7
 
 
+def test_append_refuses_half_a_pair(dsa, cache):
+    """Positions without a plan, and an output for queries that are not given, would be ignored in silence."""
+    kv, calls = cache
+    (cu, lens, table), q = batch(2, 5)
+    k = torch.zeros((5, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        kv.append(None, k, k, cu, lens, table, pos=torch.zeros((5, 1), dtype=torch.int32), stream=0)
+    with pytest.raises(ValueError):
+        kv.append(None, k, k, cu, lens, table, q, stream=0)
+    assert not calls
+    kv.append(None, k, k, cu, lens, table, stream=0)
+    assert len(calls) == 1
+
+
 def test_the_oracle_takes_keys_of_any_size():
     """The exponent of the K scale by rational arithmetic: the smallest e with x^2 + z^2 <= (448 2^e)^2."""
     def smallest(x, z):
