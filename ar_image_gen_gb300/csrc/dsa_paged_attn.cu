@@ -451,19 +451,21 @@ __device__ __forceinline__ float scale_log2(float sv)
     return (float)max((int)(u >> 23) - 127 + ((u & 0x7fffffu) != 0), kEMin);
 }
 
-// 8 columns of O^T at `col`, the terms of their weights joined.
+// 8 columns of O^T at `col`, the terms of their weights joined.  An infinity in
+// V is one in the first term's sum alone: the second, 0 or less, makes it NaN.
 template <bool FP8, int RW>
 __device__ __forceinline__ void load_out(uint32_t col, float (&x)[8])
 {
+    auto join = [](float a, float b) { return FP8 || fabsf(a) <= 3.402823466e38f ? a + b : a; };
     if constexpr (RW < 8) {  // all terms lie in 8 columns
         tmem_ld8(col, x);
 #pragma unroll
-        for (int i = 0; i < RW; ++i) x[i] += FP8 ? x[RW + i] + x[2 * RW + i] : x[RW + i];
+        for (int i = 0; i < RW; ++i) x[i] = join(x[i], FP8 ? x[RW + i] + x[2 * RW + i] : x[RW + i]);
     } else {
         float y[8];
         tmem_ld_pair(col, col + RW, x, y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] += y[i];
+        for (int i = 0; i < 8; ++i) x[i] = join(x[i], y[i]);
         if constexpr (FP8) {
             tmem_ld8(col + 2 * RW, y);
 #pragma unroll

@@ -149,6 +149,25 @@ def test_logits_far_below_zero(dsa, kv_type, Hq, Hk, new):
     attended(c, kv, values)
 
 
+@pytest.mark.parametrize("Hq,Hk,new", [(3, 3, 1), (8, 2, 1), (12, 1, 1), (8, 2, 40)])
+@pytest.mark.parametrize("n", [300, 20000])
+def test_infinities_of_attended_values(dsa, Hq, Hk, new, n):
+    """They reach the rows that attend them, as infinities, and no other element."""
+    c = Case("bf16", Hq, Hk, 64, 16, [n], [new], seed=6)
+    kv = c.cache()
+    cu, lens, table = c.batch()
+    kv.append(None, c.k.cuda(), c.v.cuda(), cu, lens, table)
+    for t, e, x in ((7, 3, "inf"), (n // 2, 9, "-inf"), (n - 45, 20, "inf"), (5, 30, "nan")):
+        kv.pages[c.table[0, t // 16], :, t % 16, 1, e] = float(x)
+    out = torch.empty_like(c.q, device="cuda")
+    kv.attend(c.q.cuda(), cu, lens, table, out, max_new=new)
+    assert kv.sync_status() == dsa.DSA_OK
+    got = out.float().cpu().numpy()
+    assert (got[:, :, [3, 20]] == np.inf).all() and (got[:, :, 9] == -np.inf).all() and np.isnan(got[:, :, 30]).all()
+    rest = [e for e in range(64) if e not in (3, 9, 20, 30)]
+    assert np.isfinite(got[:, :, rest]).all()
+
+
 # ---- after a call that gave up ----------------------------------------------
 
 @pytest.mark.parametrize("kv_type,Hq,new,n_seqs", [("bf16", 1, 1, 800), ("fp8e4m3", 1, 1, 800), ("fp8e4m3", 4, 8, 400),
