@@ -26,7 +26,7 @@ namespace dsa_rope_k {
 using namespace dsa;
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 16;  // tokens per CTA
+constexpr int kGroups = 8;  // of threads that share a token, at least
 
 struct Params {
     const int32_t *pos;
@@ -45,7 +45,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) rope_kernel(const __grid_constant__ Params p)
 {
     constexpr int L = D / 16;  // threads that cover one head
-    __shared__ float2 tab[kMaxTokens][D / 2];
+    __shared__ float2 tab[kThreads / (L * kGroups)][D / 2];
     pdl_wait();
     pdl_launch_dependents();
     const int per = L * p.groups, nt = kThreads / per;  // threads of a token, tokens of this CTA
@@ -214,13 +214,12 @@ int dsa_rope_apply(dsa_rope r, int tokens, int heads, int dtype, const int32_t *
     p.sign = inverse ? -1.f : 1.f;
     p.rope = *table;
     // A token's 8-pair runs are shared by `groups` threads: as many as there
-    // are heads while the tokens do not fill the device, else 8, so that a
+    // are heads while the tokens do not fill the device, else kGroups, so that a
     // CTA's table of sines (one entry a thread) serves 8 heads a thread.
     const int L = D / 16;
-    int most = tokens <= 1024 ? dsa_rope_k::kThreads / L : 8;
-    p.groups = 8;
+    const int most = tokens <= 1024 ? dsa_rope_k::kThreads / L : dsa_rope_k::kGroups;
+    p.groups = dsa_rope_k::kGroups;
     while (p.groups < most && p.groups < heads) p.groups *= 2;
-    while (p.groups * L * dsa_rope_k::kMaxTokens < dsa_rope_k::kThreads) p.groups *= 2;
     const int nt = dsa_rope_k::kThreads / (L * p.groups);
     const unsigned grid = (unsigned)((tokens + (long long)nt - 1) / nt);
     cudaError_t e = dtype == DSA_BF16 ? launch<__nv_bfloat16>(p, D, grid, (cudaStream_t)stream)

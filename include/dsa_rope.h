@@ -21,9 +21,10 @@
  * (x_j cos - x_j' sin, x_j' cos + x_j sin); pairs j >= r pass unchanged.
  * One axis that owns all pairs is the rotation of dsa_qkv_rope.
  *
- * Arithmetic: an angle is held as a 64-bit fraction of a turn, so it is exact
- * modulo a turn to 2^-32 turns at any int32 position; sines, cosines and the
- * rotation are fp32, rounded to the output type once.
+ * Arithmetic: base^(..) is a double, 2^-53 of it; its product with a position is
+ * held as a 64-bit fraction of a turn, exact modulo a turn to 2^-32 turns at any
+ * int32 position.  Sines and cosines are of that fraction in fp32, and they and
+ * the rotation are fp32, rounded to the output type once.
  */
 #ifndef DSA_ROPE_H
 #define DSA_ROPE_H
