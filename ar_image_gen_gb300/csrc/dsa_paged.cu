@@ -13,11 +13,12 @@
 // codes and stores.  A row is covered by D / 16 threads with 8 elements of
 // each half, so that the rotation needs no exchange.
 //
-// Measured: 8 prompts, 8200 tokens of 32 + 2 * 8 heads of 128, into E4M3 35 us
+// Measured (called): 8 prompts, 8200 tokens of 32 + 2 * 8 heads of 128, into E4M3 35 us
 // (153 MB, 0.65 of the copy bandwidth: 48% of the issue slots go to scales,
 // sines and codes, the rest waits for loads, two CTAs an SM); 7 prompts into
-// bf16, 24 + 2 * 8 heads of 64, 13.5 us (46 MB, 0.5); 96 single tokens 5.5 us,
-// a chain of dependent loads (length, page, scale, rows).
+// bf16, 24 + 2 * 8 heads of 64, 13.6 us (46 MB, 0.5); 96 single tokens 5.4 us
+// replayed from a graph (4.4 in bf16), a chain of dependent loads (length, page,
+// scale, rows).
 #include <cuda_fp8.h>
 
 #include <climits>
@@ -570,10 +571,13 @@ int dsa_paged_append(dsa_paged h, int n_seqs, int n_tokens, const int32_t *cu, c
 
     // Chunks: at most one per token, and per sequence at most one more than
     // full pages and the two ragged ends.  Heads are split over grid.y until
-    // there are two CTAs an SM (three fit; with four asked for, 96 single
-    // tokens took 9.0 us instead of 5.5 and 8.2 k prompt tokens 38 instead of
-    // 35), in parts of 8 units at least, and so that a CTA holds the scales of
-    // its parts.
+    // there are two CTAs an SM, in parts of 8 units at least, and so that a CTA
+    // holds the scales of its parts.  With four asked for instead of two (graph
+    // replays), E4M3: 96 single tokens 9.3 us instead of 5.5, 8 prompts of 1025
+    // tokens 47 instead of 54, 8.2 k ragged prompt tokens 38 instead of 35; bf16:
+    // 96 single tokens 6.7 instead of 4.4, 8 x 1025 tokens 46 instead of 41, one
+    // prompt of 2048 20.5 instead of 16.8, 7 x 700 tokens with heads of 64 13.2
+    // instead of 16.2.
     p.chunk_log2 = h->dtype == DSA_FP8_E4M3 ? h->page_log2 : 4;
     const long long bound = ((long long)n_tokens >> p.chunk_log2) + 2LL * n_seqs;
     const long long chunks = n_tokens < bound ? n_tokens : bound;

@@ -44,12 +44,12 @@
 // imbalance.)
 //
 // What bounds it: with few rows and many keys the bytes of the cache.  One new
-// token of 16 sequences of 65 to 4160 keys, 32 heads of 128, bf16: 88 us, 0.93
-// of the copy bandwidth.  96 sequences of 65 to 640 keys in E4M3: 55 us, 0.74,
-// the rest being the items' beginnings and ends (32 heads a sequence, 3 tiles
-// each on average).  One sequence is bound by latency: 10.6 us at 607 keys, of which
-// about 8 are the launch, the division of the work, the first tile and the
-// joining of its pieces.
+// token of 16 sequences of 65 to 4160 keys, 32 heads of 128, bf16: 89 us called,
+// 0.92 of the copy bandwidth.  96 sequences of 65 to 640 keys in E4M3: 56.4 us,
+// 0.73, the rest being the items' beginnings and ends (32 heads a sequence, 3
+// tiles each on average).  One sequence is bound by latency: 10.6 us at 607 keys,
+// the launch, the division of the work and a head's 5 tiles one after another in
+// one CTA (see kWhole).
 #include <cuda_fp8.h>
 #include <cudaTypedefs.h>
 
@@ -210,8 +210,15 @@ __device__ __forceinline__ int item_lead(const AttnParams &p)
 {
     return RB <= 16 ? 1 : RB == 128 ? p.lead : 12;
 }
-// An item of up to this many places is not split: it belongs to the run that
-// holds its beginning.
+// An item of up to this many places, 640 keys of single tokens, is not split: it
+// belongs to the run that holds its beginning.  A shared item's pieces are
+// published, counted and joined, which takes longer than its tiles one after
+// another, also where other CTAs are idle.  Whole and split (graph replays, 32
+// heads over 32 or 8 of 128), keys 200, 300, 640: 1 sequence over 32 in bf16 7.7,
+// 9.0, 9.5 us and 9.9, 10.4, 10.4; over 8 7.7, 8.7, 9.3 and 9.8, 10.0, 10.2; 8
+// sequences over 32 9.1, 10.7, 11.2 and 14.6, 15.7, 14.6; in E4M3 8.1, 9.2, 9.7 and
+// 13.8, 14.7, 13.4; 96 sequences in E4M3 41.8, 51.4, 80.8 and 44.6, 53.4, 82.6.
+// Items of more places are the same in both.
 template <int RB>
 constexpr int kWhole = RB <= 16 ? 6 : 0;
 template <int RB>
@@ -1309,11 +1316,11 @@ __global__ void __launch_bounds__(Shape<FP8, D, RB>::THREADS, Shape<FP8, D, RB>:
 // A tile keeps the tensor cores busy for 4 * 128 * 128 * head_dim operations
 // (540 to 1080 clocks); its softmax, read from tensor memory, counted and
 // written back, takes a warp about 2000.  That chain is the bound (16% of the
-// tensor pipe's cycles busy at heads of 64, 38% in E4M3; without the
+// tensor pipe's cycles busy at heads of 64, 36% in E4M3; without the
 // exponentials it would take 5% less): two warps a scheduler are all that the
 // registers of 64 keys a thread allow.  One sequence x 4096 tokens over 16384
-// keys, 32 heads over 8 of 128, bf16: 661 us, 1455 TFLOP/s; 32 sequences of
-// 4000 to 8196 keys x 20 to 64 rows, E4M3: 138 us, 0.44 of the copy bandwidth.
+// keys, 32 heads over 8 of 128, bf16: 660 us, 1458 TFLOP/s; 32 sequences of
+// 4000 to 8196 keys x 20 to 64 rows, E4M3: 140.9 us, 0.43 of the copy bandwidth.
 // The two halves taking whole tiles in turn, each thread a row of 128 keys,
 // took 193 us there when this form took 134.
 //
@@ -1850,12 +1857,13 @@ int with_kernel(const dsa_paged_ctx *h, int rb, Fn &&fn)
 // Row blocks: the smallest that holds max_new new tokens of a group's heads is
 // launched (128 for more).  A block of 32 is built for E4M3 only.  Its tiles
 // cost their rows, those of 128 rows the same for any number.  Heads of 128,
-// 32 over 8, block of 32 against 128: 32 sequences x 8000 keys x 20 rows 131 and
-// 158 us, 32 x 4000 x 32 rows 90 and 94, 32 x 600 x 24 rows 36 and 30, 96 x 300 x
-// 32 rows 73 and 55; heads of 64, 32 x 4000 x 24 rows 78 and 88.  In bf16 128 was
-// faster everywhere: 165 and 164 us, 96 and 94, 34.5 and 25.5, 62 and 45, 63 and
-// 58.  For 33 to 64 rows a block of 64 took longer than 128 (4 x 2000 keys x 64
-// rows: 54 us against 31 in E4M3, 45 against 27 in bf16).
+// 32 over 8, block of 32 against 128: 32 sequences x 8000 keys x 20 rows 129 and
+// 162 us, 32 x 4000 x 32 rows 89 and 97, 32 x 600 x 24 rows 34 and 29, 96 x 300 x
+// 32 rows 67 and 53; heads of 64, 32 x 4000 x 24 rows 74 and 90.  In bf16 128 was
+// faster everywhere, with weights of one term in both: 165 and 164 us, 96 and 94,
+// 34.5 and 25.5, 62 and 45, 63 and 58.  For 33 to 64 rows a block of 64 took longer
+// than 128 (4 x 2000 keys x 64 rows: 54 us against 31 in E4M3, 45 against 27 in
+// bf16).
 constexpr int kBlocks[5] = {2, 8, 16, 32, 128};
 
 int block_index(const dsa_paged_ctx *h, long long rows)

@@ -114,9 +114,11 @@ int dsa_paged_append(dsa_paged h, int n_seqs, int n_tokens, const int32_t *cu, c
  * token itself (lens and cu as for the append that came before).
  *
  * q, out: device bf16, [n_tokens, q_heads, head_dim], contiguous, 16-byte
- *     aligned, n_tokens * q_heads < 2^31; out may be q.  max_new >= 1: no sequence has more new tokens than this; a
- *     hint that only chooses the launch, any value gives the same result up
- *     to fp32 rounding order.
+ *     aligned, n_tokens * q_heads < 2^31; out may be q.
+ * max_new >= 1: no sequence has more new tokens than this; a hint that only
+ *     chooses the launch.  Any value gives the same result up to the rounding
+ *     of the weights (below) and fp32 rounding order; one far too small reads
+ *     the cache many times over.
  *
  * Slots behind a sequence's last token may hold anything (NaN included).  A
  * row whose logits hold a NaN is NaN; so are, among the new tokens of the
@@ -124,10 +126,10 @@ int dsa_paged_append(dsa_paged h, int n_seqs, int n_tokens, const int32_t *cu, c
  * Products are exact, sums and softmax statistics fp32.  For DSA_FP8_E4M3 an
  * element of q enters the first product to 8 significant bits and 2^-21 of its
  * row's largest.  The weights enter the second product with 16 significant
- * bits (DSA_BF16, where a sequence has at most 16 rows, new tokens x grouped
- * query heads), 8 (DSA_BF16 with more rows) or 9 (DSA_FP8_E4M3: also down to
- * 2^-26 of the row's largest product of a weight and its page's V scale, or less,
- * rounded), and the result is rounded to bf16 once.
+ * bits (DSA_BF16, max_new x grouped query heads at most 16), 8 (DSA_BF16, more)
+ * or 9 (DSA_FP8_E4M3; those under 2^-17 of the row's largest product of a weight
+ * and its page's V scale fewer, to 2^-26 of that product), and the result is
+ * rounded to bf16 once.
  * Deterministic for given arguments: pieces of one row are joined in the
  * order of their keys.
  * n_tokens == 0 or n_seqs == 0 is allowed.  Asynchronous on `stream`; a
