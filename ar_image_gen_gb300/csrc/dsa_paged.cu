@@ -13,10 +13,10 @@
 // codes and stores.  A row is covered by D / 16 threads with 8 elements of
 // each half, so that the rotation needs no exchange.
 //
-// Measured (called): 8 prompts, 8200 tokens of 32 + 2 * 8 heads of 128, into E4M3 35 us
-// (153 MB, 0.65 of the copy bandwidth: 48% of the issue slots go to scales,
-// sines and codes, the rest waits for loads, two CTAs an SM); 7 prompts into
-// bf16, 24 + 2 * 8 heads of 64, 13.6 us (46 MB, 0.5); 96 single tokens 5.4 us
+// Measured (called): 8 prompts, 8200 tokens of 32 + 2 * 8 heads of 128, into
+// E4M3 35.5 us (153 MB, 0.64 of the copy bandwidth: 47% of the issue slots go to
+// scales, sines and codes, the rest waits for loads, two CTAs an SM); 7 prompts
+// into bf16, 24 + 2 * 8 heads of 64, 13.6 us (46 MB, 0.5); 96 single tokens 5.4 us
 // replayed from a graph (4.4 in bf16), a chain of dependent loads (length, page,
 // scale, rows).
 #include <cuda_fp8.h>

@@ -20,12 +20,12 @@
 // t1 + t2 / 16 of two E4M3 numbers, exactly (8 = 4 + 4 significant bits) but for
 // elements under 2^-22 of its row's largest.  A weight is the sum of three E5M2
 // numbers: 9 bits, down to 2^-28 of the reference, so that thousands of keys
-// beside a dominant one keep theirs (two E4M3 numbers, 8 bits down to 2^-18, lost
-// 90 % of an output that 8200 keys of e^-13 to e^-15 made up, and took 55.9 us
-// instead of 56.2 for 96 sequences of 65 to 640 keys, 85.9 instead of 88.5 for 32 x
-// 4000 keys x 32 rows).  The scale of a
-// page and head enters the logit (K) and the weight (V); since a page's weight
-// times its scale is what is rounded, m refers to logit + log2(V scale).
+// beside a dominant one keep theirs.  (Two E4M3 numbers, 8 bits down to 2^-18,
+// lost 90 % of an output that 8200 keys of e^-13 to e^-15 made up; they took 55.9
+// us instead of 56.2 for 96 sequences of 65 to 640 keys, 85.9 instead of 88.5 for
+// 32 x 4000 keys x 32 rows.)  The scale of a page and head enters the logit (K) and
+// the weight (V); since a page's weight times its scale is what is rounded, m
+// refers to logit + log2(V scale).
 //
 // Over a bf16 cache a weight is the sum of two bf16 numbers, to 2^-16 of it, in
 // columns of their own likewise.  The second costs nothing where the cache's
