@@ -1,7 +1,7 @@
 """The paged cache at the ends of its range, against the 64-bit oracle: keys
 and V scales of any size, pages that are missing for whole tiles, tiles whose
 logits leave nothing, calls after one that gave up and beside a reading of the status,
-pools that are no device memory.  Tolerances: tests/test_gpu_paged.py, and
+pools that are no device memory or pass 32 bits, appends side by side.  Tolerances: tests/test_gpu_paged.py, and
 tests/paged_case.py for the attention.
 """
 import numpy as np
@@ -247,3 +247,51 @@ def test_a_pool_is_memory_of_the_current_device(dsa):
         assert code == dsa.DSA_ERR_ARG and not h.value and dsa.dsa_last_error()
     code, h = dsa.dsa_paged_create(1, 1, 64, 16, 1, dsa.DSA_FP8_E4M3, pages, scales)
     assert code == dsa.DSA_OK and dsa.dsa_paged_destroy(h) == dsa.DSA_OK
+
+
+# ---- large pools, calls side by side -----------------------------------------
+
+@pytest.mark.parametrize("kv_type,n_pages", [("bf16", 700000), ("fp8e4m3", 1200000)])
+@pytest.mark.parametrize("new", [1, 40])
+def test_pages_beyond_32_bits_of_bytes(dsa, kv_type, n_pages, new):
+    """A pool of 5 GB: what its last pages hold and give equals what a small pool does, bit for bit."""
+    c = Case(kv_type, 4, 1, 128, 16, [200, 77], [new, new], seed=3)
+    small = c.cache()
+    large = dsa.PagedKV(4, 1, 128, 16, n_pages, kv_type)
+    assert large.pages.numel() * large.pages.element_size() > 2 ** 32
+    large.pages[-c.n_pages:].view(torch.uint8).copy_(small.pages.view(torch.uint8))
+    if kv_type != "bf16":
+        large.scales[-c.n_pages:] = small.scales
+    cu, lens, table = c.batch()
+    far = torch.where(table >= 0, table + n_pages - c.n_pages, table)
+    outs = []
+    for kv, t in ((small, table), (large, far)):
+        kv.append(None, c.k.cuda(), c.v.cuda(), cu, lens, t)
+        outs.append(torch.empty_like(c.q, device="cuda"))
+        kv.attend(c.q.cuda(), cu, lens, t, outs[-1], max_new=new)
+        assert kv.sync_status() == dsa.DSA_OK
+    assert torch.equal(large.pages[-c.n_pages:].view(torch.uint8), small.pages.view(torch.uint8))
+    assert torch.equal(outs[0], outs[1]) and torch.isfinite(outs[0]).all()
+
+
+def test_appends_side_by_side(dsa):
+    """Two streams append to other pages of one pool through one handle."""
+    c = Case("fp8e4m3", 2, 2, 128, 16, [900, 800], [900, 800], seed=9)
+    together, apart = c.cache(), c.cache()
+    _, lens, table = c.batch()
+    k, v = c.k.cuda(), c.v.cuda()
+    together.append(None, k, v, *c.batch())
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    parts = []
+    for s in range(2):
+        a, b = int(c.cu[s]), int(c.cu[s + 1])
+        parts.append((k[a:b], v[a:b], torch.tensor([0, b - a], dtype=torch.int32, device="cuda"), lens[s:s + 1].contiguous(),
+                      table[s:s + 1].contiguous()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, part in zip(streams, parts):
+            apart.append(None, *part, stream=st)
+    torch.cuda.synchronize()
+    assert together.sync_status() == dsa.DSA_OK and apart.sync_status() == dsa.DSA_OK
+    assert torch.equal(apart.pages.view(torch.uint8), together.pages.view(torch.uint8))
+    assert torch.equal(apart.scales, together.scales)
